@@ -39,7 +39,10 @@ __all__ = [
     "SUMMARY_ALL", "SUMMARY_LAST_BLOCK", "SUMMARIES_F32", "SUMMARIES_BF16", "SUMMARIES_FP8",
     "OUT_F32", "OUT_BF16", "alloc_summaries", "fp8_summary_scales",
     "FLAG_SEQ_LEN_CLAMPED",
-    "FLAG_INDEX_SKIPPED", "FLAG_NONFINITE_SCORE", "FLAG_WAIT_TIMEOUT",
+    "FLAG_INDEX_SKIPPED", "FLAG_NONFINITE_SCORE", "FLAG_WAIT_TIMEOUT", "FLAG_NO_PAGE",
+    "ksa_assign_pages", "ksa_release_pages", "Rotary", "ksa_rotary_append_kv",
+    "ksa_rotary_append_kv_paged", "ksa_chunk_attn", "ksa_chunk_attn_paged",
+    "ksa_chunk_attn_workspace", "MASK_NONE", "MASK_CAUSAL",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -50,6 +53,8 @@ SUMMARIES_F32, SUMMARIES_BF16, SUMMARIES_FP8 = 0, 1, 2
 IDX_PER_KV_HEAD, IDX_SHARED, IDX_PER_Q_HEAD = 0, 1, 2
 OUT_F32, OUT_BF16 = 0, 1
 FLAG_SEQ_LEN_CLAMPED, FLAG_INDEX_SKIPPED, FLAG_NONFINITE_SCORE, FLAG_WAIT_TIMEOUT = 1, 2, 4, 8
+FLAG_NO_PAGE = 16
+MASK_NONE, MASK_CAUSAL = 0, 1
 _STATUS = {0: "KSA_OK", 1: "KSA_ERR_INVALID_ARG", 2: "KSA_ERR_UNSUPPORTED",
            3: "KSA_ERR_WORKSPACE", 4: "KSA_ERR_CUDA"}
 
@@ -72,6 +77,12 @@ class Pages(ctypes.Structure):
     """ksa_pages: the block table of a paged K/V cache (page = block)."""
     _fields_ = [("block_table", ctypes.c_void_p), ("max_blocks", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32)]
+
+
+class _RotaryStruct(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+                ("axis_of_pair", ctypes.POINTER(ctypes.c_int32))]
 
 
 _vp, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
@@ -119,6 +130,23 @@ _SIGS = {
     "ksa_unified_select_workspace": (_sz, [ctypes.POINTER(Shape), _i32, _i32]),
     "ksa_unified_select": (_i32, [ctypes.POINTER(Shape), _vp, _vp, _vp, _i32, _i32, _i32, _vp,
                                   _vp, _vp, _sz, _vp, _vp]),
+    "ksa_assign_pages": (_i32, [ctypes.POINTER(Shape), _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp,
+                                _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "ksa_release_pages": (_i32, [ctypes.POINTER(Shape), _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp,
+                                 _sz, _vp, _vp]),
+    "ksa_rotary_append_kv": (_i32, [ctypes.POINTER(Shape), _i32, ctypes.POINTER(_RotaryStruct),
+                                    _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp,
+                                    _vp, _vp, _vp]),
+    "ksa_rotary_append_kv_paged": (_i32, [ctypes.POINTER(Shape), _i32,
+                                          ctypes.POINTER(_RotaryStruct), _vp, _i32, _vp, _i32,
+                                          _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp,
+                                          _vp]),
+    "ksa_chunk_attn_workspace": (_sz, [ctypes.POINTER(Shape), _i32]),
+    "ksa_chunk_attn": (_i32, [ctypes.POINTER(Shape), _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32,
+                              _f32, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "ksa_chunk_attn_paged": (_i32, [ctypes.POINTER(Shape), _i32, _vp, _i32, _vp, _vp,
+                                    ctypes.POINTER(Pages), _vp, _vp, _i32, _f32, _vp, _vp, _vp,
+                                    _sz, _vp, _vp]),
     "ksa_status_string": (ctypes.c_char_p, [_i32]),
     "ksa_last_error": (ctypes.c_char_p, []),
     "ksa_version": (_i32, []),
@@ -737,6 +765,328 @@ def ksa_select_tokens_one_head(q: torch.Tensor, K: torch.Tensor, seq_lens: torch
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
         _stream(stream)))
     return token_idx, num_sel
+
+
+# ---------------------------------------------------------------------------
+# paged serving: page assignment, rotary cache writes, attention of query chunks
+
+
+def _same_device(first: torch.Tensor, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+
+
+def _sized(t: torch.Tensor, name: str, shape) -> None:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _run_on(t: torch.Tensor, stream, fn, *args) -> None:
+    """One library call on t's device, on `stream` or that device's current stream."""
+    if t.device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(t.device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _scratch(ws: Optional[torch.Tensor], need: int, like: torch.Tensor) -> torch.Tensor:
+    if ws is None:
+        return torch.zeros((max(int(need), 256),), dtype=torch.uint8, device=like.device)
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    return ws
+
+
+def ksa_assign_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                     free_pages: torch.Tensor, num_free: torch.Tensor, block_size: int,
+                     num_tokens: int, num_free_out: Optional[torch.Tensor] = None,
+                     seq_lens: Optional[torch.Tensor] = None,
+                     cu_new: Optional[torch.Tensor] = None,
+                     slots: Optional[torch.Tensor] = None,
+                     positions: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Pages and slots for every row's new tokens: (seq_lens [B], cu_new [B+1], slots
+    [num_tokens] int64, positions [num_tokens]).  block_table [B, max_blocks] gets the new
+    blocks' pages, taken off the top of the stack free_pages [num_pages]; num_free [1] is
+    updated in place unless num_free_out is given.  seq_lens may be ctx_lens."""
+    _dev(ctx_lens, "ctx_lens", torch.int32)
+    _dev(new_lens, "new_lens", torch.int32)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(free_pages, "free_pages", torch.int32)
+    _dev(num_free, "num_free", torch.int32)
+    B, mb = block_table.shape
+    dev = block_table.device
+    if num_free_out is None:
+        num_free_out = num_free
+    if seq_lens is None:
+        seq_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    if cu_new is None:
+        cu_new = torch.empty((B + 1,), dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty((num_tokens,), dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty((num_tokens,), dtype=torch.int32, device=dev)
+    _dev(num_free_out, "num_free_out", torch.int32)
+    _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(cu_new, "cu_new", torch.int32)
+    _dev(slots, "slots", torch.int64)
+    _dev(positions, "positions", torch.int32)
+    for t, name, shape in ((ctx_lens, "ctx_lens", (B,)), (new_lens, "new_lens", (B,)),
+                           (seq_lens, "seq_lens", (B,)), (cu_new, "cu_new", (B + 1,)),
+                           (num_free, "num_free", (1,)), (num_free_out, "num_free_out", (1,)),
+                           (slots, "slots", (num_tokens,)),
+                           (positions, "positions", (num_tokens,))):
+        _sized(t, name, shape)
+    ws = _scratch(workspace, 256, block_table)
+    _same_device(block_table, ctx_lens, new_lens, free_pages, num_free, num_free_out, seq_lens,
+                 cu_new, slots, positions, ws, dev_status)
+    sh = _shape(B, 1, 1, 64, mb * block_size, block_size)
+    _run_on(block_table, stream, lib().ksa_assign_pages, ctypes.byref(sh), _ptr(ctx_lens),
+            _ptr(new_lens), _ptr(block_table), mb, free_pages.numel(), _ptr(free_pages),
+            _ptr(num_free), _ptr(num_free_out), int(num_tokens), _ptr(seq_lens), _ptr(cu_new),
+            _ptr(slots), _ptr(positions), _ptr(ws), ws.numel() * ws.element_size(),
+            _ptr(dev_status))
+    return seq_lens, cu_new, slots, positions
+
+
+def ksa_release_pages(seq_lens: torch.Tensor, done: torch.Tensor, block_table: torch.Tensor,
+                      free_pages: torch.Tensor, num_free: torch.Tensor, block_size: int,
+                      workspace: Optional[torch.Tensor] = None,
+                      dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows with done[b] != 0 give their pages back to the stack (free_pages, num_free); their
+    table entries become -1 and their seq_lens 0, all in place."""
+    _dev(seq_lens, "seq_lens", torch.int32)
+    _dev(done, "done", torch.int32)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(free_pages, "free_pages", torch.int32)
+    _dev(num_free, "num_free", torch.int32)
+    B, mb = block_table.shape
+    _sized(seq_lens, "seq_lens", (B,))
+    _sized(done, "done", (B,))
+    _sized(num_free, "num_free", (1,))
+    ws = _scratch(workspace, 256, block_table)
+    _same_device(block_table, seq_lens, done, free_pages, num_free, ws, dev_status)
+    sh = _shape(B, 1, 1, 64, mb * block_size, block_size)
+    _run_on(block_table, stream, lib().ksa_release_pages, ctypes.byref(sh), _ptr(done),
+            _ptr(seq_lens), _ptr(block_table), mb, free_pages.numel(), _ptr(free_pages),
+            _ptr(num_free), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status))
+
+
+class Rotary:
+    """Rotary positions of a model: inv_freq (P host values; the leading 2P dims of a head turn),
+    the axis of each pair (None: one axis), and whether pairs are neighbours (interleaved) or
+    P dims apart.  Made once, passed to every ksa_rotary_append_kv call."""
+
+    def __init__(self, inv_freq, axis_of_pair=None, interleaved: bool = False,
+                 num_axes: Optional[int] = None):
+        as_list = lambda x: x.tolist() if hasattr(x, "tolist") else list(x)
+        freq = [float(f) for f in as_list(inv_freq)]
+        P = len(freq)
+        self.num_axes = 1 if num_axes is None else int(num_axes)
+        self._freq = (ctypes.c_double * max(P, 1))(*freq)
+        self._axis = None
+        if axis_of_pair is not None:
+            axis = [int(i) for i in as_list(axis_of_pair)]
+            if len(axis) != P:
+                raise ValueError(f"axis_of_pair must hold {P} axes, got {len(axis)}")
+            self._axis = (ctypes.c_int32 * max(P, 1))(*axis)
+            if num_axes is None:
+                self.num_axes = max(axis) + 1 if axis else 1
+        self.rotary_dim = 2 * P
+        self._struct = _RotaryStruct(
+            2 * P, self.num_axes, int(bool(interleaved)), self._freq,
+            self._axis if self._axis is not None else ctypes.POINTER(ctypes.c_int32)())
+        self._ref = ctypes.byref(self._struct)
+
+
+def _token_rows(t: torch.Tensor, name: str) -> int:
+    """Checks a [N, heads, D] bf16 tensor whose heads and dims are dense; its token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    n, s1, s2 = t.stride()
+    h, d = t.shape[1], t.shape[2]
+    if s2 != 1 or (h > 1 and s1 != d):
+        raise ValueError(f"{name}: the heads and dims of a token must be dense")
+    if n >= 1 << 31:
+        raise ValueError(f"{name}: a token stride of 2^31 elements or more")
+    return n if t.shape[0] > 1 else h * d
+
+
+def _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged, dev_status, stream):
+    kv = k is not None
+    if kv != (v is not None) or kv != (K is not None) or kv != (V is not None):
+        raise ValueError("k, v, K and V must be given together")
+    if q is None and not kv:
+        raise ValueError("neither queries nor keys and values are given")
+    if rotary is None and q is not None:
+        raise ValueError("q needs a Rotary")
+    lead = q if q is not None else k
+    qs = ks = vs = os_ = 0
+    N, D = lead.shape[0], lead.shape[-1]
+    if q is not None:
+        qs = _token_rows(q, "q")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        os_ = _token_rows(q_out, "q_out")
+        _sized(q_out, "q_out", q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    Hkv, B, T, bs, num_pages = 1, 1, 1, 16, 0
+    if kv:
+        ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
+        _dev(K, "K", torch.bfloat16)
+        _dev(V, "V", torch.bfloat16)
+        _sized(k, "k", (N, K.shape[1], D))
+        _sized(v, "v", k.shape)
+        _sized(V, "V", K.shape)
+        Hkv = K.shape[1]
+        if K.dim() != 4 or K.shape[3] != D:
+            raise ValueError(f"K and V must be 4-dimensional with {D} dims a head")
+        if paged:
+            num_pages, bs = K.shape[0], K.shape[2]
+            T = bs
+        else:
+            B, T = K.shape[0], K.shape[2]
+        if slots is None:
+            raise ValueError("slots must be given with k and v")
+    if slots is not None:
+        _dev(slots, "slots", torch.int64)
+        _sized(slots, "slots", (N,))
+    if rotary is not None:
+        _dev(positions, "positions", torch.int32)
+        if positions.dim() == 1:
+            positions = positions[None]
+        _sized(positions, "positions", (rotary.num_axes, N))
+    _same_device(lead, k, v, slots, K, V, q_out, dev_status)
+    if rotary is not None:
+        _same_device(lead, positions)
+    Hq = q.shape[1] if q is not None else Hkv
+    if not kv:
+        Hkv = Hq
+    sh = _shape(B, Hq, Hkv, D, T, bs)
+    ref = rotary._ref if rotary is not None else None
+    args = (ctypes.byref(sh), N, ref, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+            _ptr(positions) if rotary is not None else None, _ptr(slots), _ptr(q_out), os_,
+            _ptr(K), _ptr(V))
+    if paged:
+        _run_on(lead, stream, lib().ksa_rotary_append_kv_paged, *args, num_pages,
+                _ptr(dev_status))
+    else:
+        _run_on(lead, stream, lib().ksa_rotary_append_kv, *args, _ptr(dev_status))
+    return q_out
+
+
+def ksa_rotary_append_kv(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                         v: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                         slots: Optional[torch.Tensor], K: Optional[torch.Tensor],
+                         V: Optional[torch.Tensor], rotary: Optional[Rotary],
+                         q_out: Optional[torch.Tensor] = None,
+                         dev_status: Optional[torch.Tensor] = None, stream=None):
+    """q_out = rotated q [N, Hq, D]; the rotated k and v [N, Hkv, D] go to slot b * T + t of the
+    caches K, V [B, Hkv, T, D] (slots [N] int64, negative: padding, the token is skipped).
+    positions: [axes, N] int32 (or [N]).  q, k, v may be strided by token (columns of a fused
+    projection).  q None: keys and values only; K None: queries only; rotary None: k and v as
+    they are."""
+    return _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, False, dev_status,
+                          stream)
+
+
+def ksa_rotary_append_kv_paged(q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                               v: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                               slots: Optional[torch.Tensor], K_pages: Optional[torch.Tensor],
+                               V_pages: Optional[torch.Tensor], rotary: Optional[Rotary],
+                               q_out: Optional[torch.Tensor] = None,
+                               dev_status: Optional[torch.Tensor] = None, stream=None):
+    """ksa_rotary_append_kv into page pools [num_pages, Hkv, bs, D]: slot = page * bs + offset
+    (the slots of ksa_assign_pages)."""
+    return _rotary_append(q, k, v, positions, slots, K_pages, V_pages, rotary, q_out, True,
+                          dev_status, stream)
+
+
+def ksa_chunk_attn_workspace(B: int, Hq: int, Hkv: int, D: int, T: int, num_tokens: int) -> int:
+    sh = _shape(B, Hq, Hkv, D, T)
+    return int(lib().ksa_chunk_attn_workspace(ctypes.byref(sh), int(num_tokens)))
+
+
+def _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse, workspace,
+                dev_status, stream):
+    qs = _token_rows(q, "q")
+    _dev(K, "K", torch.bfloat16)
+    _dev(V, "V", torch.bfloat16)
+    _dev(cu_q, "cu_q", torch.int32)
+    _dev(seq_lens, "seq_lens", torch.int32)
+    N, Hq, D = q.shape
+    if K.dim() != 4 or K.shape[3] != D:
+        raise ValueError(f"K and V must be 4-dimensional with {D} dims a head")
+    _sized(V, "V", K.shape)
+    Hkv, bs = K.shape[1], 16
+    if block_table is not None:
+        _dev(block_table, "block_table", torch.int32)
+        B, mb = block_table.shape
+        bs = K.shape[2]
+        T = mb * bs
+    else:
+        B, T = K.shape[0], K.shape[2]
+    _sized(seq_lens, "seq_lens", (B,))
+    _sized(cu_q, "cu_q", (B + 1,))
+    if out is None:
+        out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+    _dev(out, "out", torch.bfloat16)
+    _sized(out, "out", q.shape)
+    if lse is not None:
+        _dev(lse, "lse", torch.float32)
+        _sized(lse, "lse", (N, Hq))
+    sh = _shape(B, Hq, Hkv, D, T, bs)
+    ws = workspace
+    if ws is None:
+        with torch.cuda.device(q.device):
+            need = lib().ksa_chunk_attn_workspace(ctypes.byref(sh), N)
+        ws = _scratch(None, need, q)
+    ws = _scratch(ws, 0, q)
+    _same_device(q, K, V, block_table, cu_q, seq_lens, out, lse, ws, dev_status)
+    rest = (_ptr(cu_q), _ptr(seq_lens), int(mask), float(scale), _ptr(out), _ptr(lse), _ptr(ws),
+            ws.numel() * ws.element_size(), _ptr(dev_status))
+    if block_table is not None:
+        pg = _pages(block_table, K.shape[0])
+        _run_on(q, stream, lib().ksa_chunk_attn_paged, ctypes.byref(sh), N, _ptr(q), qs, _ptr(K),
+                _ptr(V), ctypes.byref(pg), *rest)
+    else:
+        _run_on(q, stream, lib().ksa_chunk_attn, ctypes.byref(sh), N, _ptr(q), qs, _ptr(K),
+                _ptr(V), *rest)
+    return out, lse
+
+
+def ksa_chunk_attn(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.Tensor,
+                   seq_lens: torch.Tensor, mask: int = MASK_CAUSAL, scale: float = 0.0,
+                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None,
+                   dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of row b's queries q[cu_q[b]:cu_q[b+1]] ([N, Hq, D]) over its seq_lens[b] cached
+    tokens in K, V [B, Hkv, T, D]: (out [N, Hq, D] bf16, lse).  MASK_CAUSAL: the queries are the
+    row's newest tokens; MASK_NONE: every query sees every token (an encoder's states)."""
+    return _chunk_attn(q, K, V, None, cu_q, seq_lens, mask, scale, out, lse, workspace,
+                       dev_status, stream)
+
+
+def ksa_chunk_attn_paged(q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tensor,
+                         block_table: torch.Tensor, cu_q: torch.Tensor, seq_lens: torch.Tensor,
+                         mask: int = MASK_CAUSAL, scale: float = 0.0,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None,
+                         dev_status: Optional[torch.Tensor] = None, stream=None):
+    """ksa_chunk_attn on a paged K/V cache (pools [num_pages, Hkv, bs, D], block table
+    [B, max_blocks])."""
+    if block_table is None:
+        raise TypeError("block_table must be a CUDA tensor")
+    return _chunk_attn(q, K_pages, V_pages, block_table, cu_q, seq_lens, mask, scale, out, lse,
+                       workspace, dev_status, stream)
 
 
 def ksa_get_device_status(dev_status: torch.Tensor, clear: bool = False, stream=None) -> int:

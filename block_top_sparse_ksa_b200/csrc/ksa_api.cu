@@ -781,6 +781,335 @@ ksa_status ksa_select_tokens_one_head(const ksa_shape *shape, const uint16_t *q,
   return KSA_OK;
 }
 
+// ---------------------------------------------------------------------------
+// paged serving: page assignment, rotary cache writes, chunk attention
+
+namespace {
+
+// Shape, table and pool of the two page calls.
+ksa_status check_page_call(const ksa_shape *shape, const void *block_table, int32_t max_blocks,
+                           int32_t num_pages, const void *free_pages, const void *num_free,
+                           const void *ws, size_t ws_bytes) {
+  ksa_status st = check_shape(shape, true);
+  if (st != KSA_OK) return st;
+  if (block_table == nullptr || free_pages == nullptr || num_free == nullptr)
+    return fail(KSA_ERR_INVALID_ARG, "block_table, free_pages and num_free must be non-NULL");
+  if (max_blocks < 1 || num_pages < 1)
+    return fail(KSA_ERR_INVALID_ARG, "max_blocks and num_pages must be >= 1");
+  if (static_cast<long long>(max_blocks) * shape->block_size != shape->capacity)
+    return fail(KSA_ERR_INVALID_ARG, "capacity %d must equal max_blocks * block_size (%d * %d)",
+                shape->capacity, max_blocks, shape->block_size);
+  if (!aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(num_free, 4))
+    return fail(KSA_ERR_INVALID_ARG, "block_table, free_pages and num_free must be aligned");
+  if (ws == nullptr || ws_bytes < 256 || !aligned(ws, 256))
+    return fail(KSA_ERR_WORKSPACE, "workspace: 256 bytes, 256-byte aligned, are needed");
+  return KSA_OK;
+}
+
+}  // namespace
+
+ksa_status ksa_assign_pages(const ksa_shape *shape, const int32_t *ctx_lens,
+                            const int32_t *new_lens, int32_t *block_table, int32_t max_blocks,
+                            int32_t num_pages, const int32_t *free_pages,
+                            const int32_t *num_free, int32_t *num_free_out,
+                            int32_t num_tokens, int32_t *seq_lens, int32_t *cu_new,
+                            int64_t *slots, int32_t *positions, void *ws, size_t ws_bytes,
+                            uint32_t *dev_status, void *stream) {
+  ksa_status st = check_page_call(shape, block_table, max_blocks, num_pages, free_pages,
+                                  num_free, ws, ws_bytes);
+  if (st != KSA_OK) return st;
+  if (ctx_lens == nullptr || new_lens == nullptr || num_free_out == nullptr ||
+      seq_lens == nullptr || cu_new == nullptr)
+    return fail(KSA_ERR_INVALID_ARG,
+                "ctx_lens, new_lens, num_free_out, seq_lens and cu_new must be non-NULL");
+  if (num_tokens < 0 || num_tokens >= (1 << 30))
+    return fail(KSA_ERR_INVALID_ARG, "num_tokens %d is not in [0, 2^30)", num_tokens);
+  if (num_tokens > 0 && (slots == nullptr || positions == nullptr))
+    return fail(KSA_ERR_INVALID_ARG, "slots and positions must be non-NULL");
+  if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(num_free_out, 4) ||
+      !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(slots, 8) ||
+      !aligned(positions, 4))
+    return fail(KSA_ERR_INVALID_ARG, "slots must be 8-byte aligned, the other arrays 4-byte");
+  ksa::AssignArgs a;
+  a.ctx_lens = ctx_lens;
+  a.new_lens = new_lens;
+  a.block_table = block_table;
+  a.free_pages = free_pages;
+  a.num_free = num_free;
+  a.num_free_out = num_free_out;
+  a.seq_lens = seq_lens;
+  a.cu_new = cu_new;
+  a.slots = slots;
+  a.positions = positions;
+  a.counter = static_cast<uint32_t *>(ws);
+  a.status = dev_status;
+  a.B = shape->batch;
+  a.T = shape->capacity;
+  a.bs = shape->block_size;
+  a.max_blocks = max_blocks;
+  a.num_pages = num_pages;
+  a.N = num_tokens;
+  return cuda_status(ksa::launch_assign_pages(a, static_cast<cudaStream_t>(stream)),
+                     "ksa_assign_pages launch");
+}
+
+ksa_status ksa_release_pages(const ksa_shape *shape, const int32_t *done, int32_t *seq_lens,
+                             int32_t *block_table, int32_t max_blocks, int32_t num_pages,
+                             int32_t *free_pages, int32_t *num_free, void *ws,
+                             size_t ws_bytes, uint32_t *dev_status, void *stream) {
+  ksa_status st = check_page_call(shape, block_table, max_blocks, num_pages, free_pages,
+                                  num_free, ws, ws_bytes);
+  if (st != KSA_OK) return st;
+  if (done == nullptr || seq_lens == nullptr)
+    return fail(KSA_ERR_INVALID_ARG, "done and seq_lens must be non-NULL");
+  if (!aligned(done, 4) || !aligned(seq_lens, 4))
+    return fail(KSA_ERR_INVALID_ARG, "done and seq_lens must be 4-byte aligned");
+  ksa::ReleaseArgs a;
+  a.done = done;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.free_pages = free_pages;
+  a.num_free = num_free;
+  a.counter = static_cast<uint32_t *>(ws);
+  a.status = dev_status;
+  a.B = shape->batch;
+  a.T = shape->capacity;
+  a.bs = shape->block_size;
+  a.max_blocks = max_blocks;
+  a.num_pages = num_pages;
+  return cuda_status(
+      ksa::launch_release_pages(a, device_sm_count(), static_cast<cudaStream_t>(stream)),
+      "ksa_release_pages launch");
+}
+
+namespace {
+
+// `paged`: slots are page * block_size + offset in a pool of num_pages.
+ksa_status rotary_common(const ksa_shape *shape, int32_t num_tokens, const ksa_rotary *rotary,
+                         const uint16_t *q, int32_t q_stride, const uint16_t *k,
+                         int32_t k_stride, const uint16_t *v, int32_t v_stride,
+                         const int32_t *positions, const int64_t *slots, uint16_t *q_out,
+                         int32_t q_out_stride, uint16_t *K, uint16_t *V, bool paged,
+                         int32_t num_pages, uint32_t *dev_status, void *stream) {
+  ksa_status st = check_shape(shape, paged);
+  if (st != KSA_OK) return st;
+  if (num_tokens < 0 || num_tokens >= (1 << 30))
+    return fail(KSA_ERR_INVALID_ARG, "num_tokens %d is not in [0, 2^30)", num_tokens);
+  const bool kv = K != nullptr;
+  if (kv && paged) {
+    if (num_pages < 1) return fail(KSA_ERR_INVALID_ARG, "num_pages must be >= 1");
+    if (static_cast<long long>(num_pages) * shape->num_kv_heads * shape->block_size >=
+        (1LL << 31))
+      return fail(KSA_ERR_UNSUPPORTED, "num_pages * num_kv_heads * block_size must be < 2^31");
+  }
+  const int D = shape->head_dim, P = rotary != nullptr ? rotary->rotary_dim / 2 : 0;
+  if (rotary != nullptr) {
+    if (rotary->rotary_dim < 16 || rotary->rotary_dim > D || rotary->rotary_dim % 16 != 0)
+      return fail(KSA_ERR_INVALID_ARG, "rotary_dim %d is not a multiple of 16 in [16, %d]",
+                  rotary->rotary_dim, D);
+    if (rotary->num_axes < 1 || rotary->num_axes > 8)
+      return fail(KSA_ERR_INVALID_ARG, "num_axes %d is not in [1, 8]", rotary->num_axes);
+    if (rotary->interleaved != 0 && rotary->interleaved != 1)
+      return fail(KSA_ERR_INVALID_ARG, "interleaved %d is neither 0 nor 1", rotary->interleaved);
+    if (rotary->inv_freq == nullptr)
+      return fail(KSA_ERR_INVALID_ARG, "rotary->inv_freq must be non-NULL");
+    for (int i = 0; i < P; ++i) {
+      if (!isfinite(rotary->inv_freq[i]))
+        return fail(KSA_ERR_INVALID_ARG, "inv_freq[%d] is not finite", i);
+      if (rotary->axis_of_pair != nullptr && (rotary->axis_of_pair[i] < 0 ||
+                                              rotary->axis_of_pair[i] >= rotary->num_axes))
+        return fail(KSA_ERR_INVALID_ARG, "axis_of_pair[%d] = %d is not in [0, %d)", i,
+                    rotary->axis_of_pair[i], rotary->num_axes);
+    }
+  }
+  if (num_tokens == 0) {
+    g_last_error.clear();
+    return KSA_OK;
+  }
+  if ((q == nullptr) != (q_out == nullptr))
+    return fail(KSA_ERR_INVALID_ARG, "q and q_out must be given together");
+  if ((k == nullptr) == kv || (v == nullptr) == kv || (V == nullptr) == kv)
+    return fail(KSA_ERR_INVALID_ARG, "k, v, K and V must be given together");
+  if (q == nullptr && !kv)
+    return fail(KSA_ERR_INVALID_ARG, "neither queries nor keys and values are given");
+  if (kv && slots == nullptr) return fail(KSA_ERR_INVALID_ARG, "slots must be non-NULL");
+  if (rotary != nullptr && positions == nullptr)
+    return fail(KSA_ERR_INVALID_ARG, "positions must be non-NULL");
+  if (rotary == nullptr && q != nullptr)
+    return fail(KSA_ERR_INVALID_ARG, "q needs a rotary");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(K, 16) || !aligned(V, 16))
+    return fail(KSA_ERR_INVALID_ARG, "q, k, v, q_out, K and V must be 16-byte aligned");
+  if (!aligned(positions, 4) || !aligned(slots, 8))
+    return fail(KSA_ERR_INVALID_ARG, "positions must be 4-byte aligned, slots 8-byte");
+  const int64_t q_row = static_cast<int64_t>(shape->num_q_heads) * D,
+                kv_row = static_cast<int64_t>(shape->num_kv_heads) * D;
+  if ((q != nullptr && (q_stride < q_row || q_stride % 8 != 0 || q_out_stride < q_row ||
+                        q_out_stride % 8 != 0)) ||
+      (kv && (k_stride < kv_row || k_stride % 8 != 0 || v_stride < kv_row || v_stride % 8 != 0)))
+    return fail(KSA_ERR_INVALID_ARG,
+                "token strides must be multiples of 8 elements and hold the token's heads");
+  if (q == q_out && q != nullptr && q_stride != q_out_stride)
+    return fail(KSA_ERR_INVALID_ARG, "q_out may be q only with the same stride");
+  ksa::RotaryArgs a;
+  memset(&a, 0, sizeof a);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out = q_out;
+  a.K = K;
+  a.V = V;
+  a.positions = positions;
+  a.slots = slots;
+  a.status = dev_status;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out_stride = q_out_stride;
+  a.slots_per_page = paged ? shape->block_size : shape->capacity;
+  a.num_slots = !kv ? INT32_MAX
+                    : static_cast<long long>(a.slots_per_page) * (paged ? num_pages : shape->batch);
+  a.N = num_tokens;
+  a.Hq = shape->num_q_heads;
+  a.Hkv = shape->num_kv_heads;
+  a.D = D;
+  a.rotary_dim = 2 * P;
+  a.interleaved = rotary != nullptr ? rotary->interleaved : 0;
+  for (int i = 0; i < P; ++i) {
+    a.turns_per_step[i] = rotary->inv_freq[i] / 6.283185307179586476925286766559;
+    a.axis[i] = rotary->axis_of_pair != nullptr
+                    ? static_cast<uint8_t>(rotary->axis_of_pair[i])
+                    : static_cast<uint8_t>(0);
+  }
+  return cuda_status(
+      ksa::launch_rotary_append(a, device_sm_count(), static_cast<cudaStream_t>(stream)),
+      "ksa_rotary_append_kv launch");
+}
+
+}  // namespace
+
+ksa_status ksa_rotary_append_kv(const ksa_shape *shape, int32_t num_tokens,
+                                const ksa_rotary *rotary, const uint16_t *q, int32_t q_stride,
+                                const uint16_t *k, int32_t k_stride, const uint16_t *v,
+                                int32_t v_stride, const int32_t *positions,
+                                const int64_t *slots, uint16_t *q_out, int32_t q_out_stride,
+                                uint16_t *K, uint16_t *V, uint32_t *dev_status, void *stream) {
+  return rotary_common(shape, num_tokens, rotary, q, q_stride, k, k_stride, v, v_stride,
+                       positions, slots, q_out, q_out_stride, K, V, false, 0, dev_status,
+                       stream);
+}
+
+ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens,
+                                      const ksa_rotary *rotary, const uint16_t *q,
+                                      int32_t q_stride, const uint16_t *k, int32_t k_stride,
+                                      const uint16_t *v, int32_t v_stride,
+                                      const int32_t *positions, const int64_t *slots,
+                                      uint16_t *q_out, int32_t q_out_stride,
+                                      uint16_t *K_pages, uint16_t *V_pages, int32_t num_pages,
+                                      uint32_t *dev_status, void *stream) {
+  return rotary_common(shape, num_tokens, rotary, q, q_stride, k, k_stride, v, v_stride,
+                       positions, slots, q_out, q_out_stride, K_pages, V_pages, true, num_pages,
+                       dev_status, stream);
+}
+
+namespace {
+
+ksa_status check_chunk(const ksa_shape *shape, bool paged, int32_t num_tokens) {
+  ksa_status st = check_shape(shape, paged);
+  if (st != KSA_OK) return st;
+  if (num_tokens < 0) return fail(KSA_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (shape->num_q_heads / shape->num_kv_heads > 128)
+    return fail(KSA_ERR_UNSUPPORTED, "more than 128 query heads per kv-head");
+  if (static_cast<long long>(num_tokens) * shape->num_q_heads >= (1LL << 31))
+    return fail(KSA_ERR_UNSUPPORTED, "num_tokens * num_q_heads must be < 2^31");
+  return KSA_OK;
+}
+
+ksa_status chunk_common(const ksa_shape *shape, int32_t num_tokens, const uint16_t *q,
+                        int32_t q_stride, const uint16_t *K, const uint16_t *V,
+                        const ksa_pages *pages, bool paged, const int32_t *cu_q,
+                        const int32_t *seq_lens, int32_t mask, float scale, uint16_t *out,
+                        float *lse, void *ws, size_t ws_bytes, uint32_t *dev_status,
+                        void *stream) {
+  ksa_status st = check_chunk(shape, paged, num_tokens);
+  if (st != KSA_OK) return st;
+  ksa::ChunkArgs a;
+  if (paged && (st = check_pages(shape, pages, &a.kv)) != KSA_OK) return st;
+  if (mask != KSA_MASK_NONE && mask != KSA_MASK_CAUSAL)
+    return fail(KSA_ERR_INVALID_ARG, "mask %d is neither NONE nor CAUSAL", mask);
+  if (!(scale >= 0.f) || isinf(scale))
+    return fail(KSA_ERR_INVALID_ARG, "scale must be finite and >= 0 (0 selects 1/sqrt(D))");
+  if (num_tokens == 0) {
+    g_last_error.clear();
+    return KSA_OK;
+  }
+  if (q == nullptr || K == nullptr || V == nullptr || cu_q == nullptr || seq_lens == nullptr ||
+      out == nullptr)
+    return fail(KSA_ERR_INVALID_ARG, "q, K, V, cu_q, seq_lens and out must be non-NULL");
+  if (!aligned(q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(out, 16))
+    return fail(KSA_ERR_INVALID_ARG, "q, K, V and out must be 16-byte aligned");
+  if (!aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4))
+    return fail(KSA_ERR_INVALID_ARG, "cu_q, seq_lens and lse must be 4-byte aligned");
+  if (q_stride < static_cast<int64_t>(shape->num_q_heads) * shape->head_dim || q_stride % 8 != 0)
+    return fail(KSA_ERR_INVALID_ARG,
+                "q_stride must be a multiple of 8 elements that holds the token's heads");
+  const int sms = device_sm_count();
+  const size_t need = ksa::chunk_attn_workspace_bytes(shape->batch, shape->num_q_heads,
+                                                      shape->num_kv_heads, shape->head_dim,
+                                                      shape->capacity, num_tokens, sms);
+  if (ws == nullptr || ws_bytes < need || !aligned(ws, 256))
+    return fail(KSA_ERR_WORKSPACE, "workspace: %zu bytes, 256-byte aligned, are needed (%zu given)",
+                need, ws == nullptr ? static_cast<size_t>(0) : ws_bytes);
+  a.q = q;
+  a.K = K;
+  a.V = V;
+  a.cu_q = cu_q;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.lse = lse;
+  a.status = dev_status;
+  a.q_stride = q_stride;
+  a.B = shape->batch;
+  a.Hq = shape->num_q_heads;
+  a.Hkv = shape->num_kv_heads;
+  a.D = shape->head_dim;
+  a.T = shape->capacity;
+  a.N = num_tokens;
+  a.causal = mask == KSA_MASK_CAUSAL;
+  a.scale = scale == 0.f ? static_cast<float>(1.0 / sqrt(static_cast<double>(shape->head_dim)))
+                         : scale;
+  return cuda_status(ksa::launch_chunk_attn(a, ws, sms, static_cast<cudaStream_t>(stream)),
+                     "ksa_chunk_attn launch");
+}
+
+}  // namespace
+
+size_t ksa_chunk_attn_workspace(const ksa_shape *shape, int32_t num_tokens) {
+  if (check_chunk(shape, false, num_tokens) != KSA_OK) return 0;
+  return ksa::chunk_attn_workspace_bytes(shape->batch, shape->num_q_heads, shape->num_kv_heads,
+                                         shape->head_dim, shape->capacity, num_tokens,
+                                         device_sm_count());
+}
+
+ksa_status ksa_chunk_attn(const ksa_shape *shape, int32_t num_tokens, const uint16_t *q,
+                          int32_t q_stride, const uint16_t *K, const uint16_t *V,
+                          const int32_t *cu_q, const int32_t *seq_lens, int32_t mask,
+                          float scale, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
+                          uint32_t *dev_status, void *stream) {
+  return chunk_common(shape, num_tokens, q, q_stride, K, V, nullptr, false, cu_q, seq_lens, mask,
+                      scale, out, lse, ws, ws_bytes, dev_status, stream);
+}
+
+ksa_status ksa_chunk_attn_paged(const ksa_shape *shape, int32_t num_tokens, const uint16_t *q,
+                                int32_t q_stride, const uint16_t *K_pages,
+                                const uint16_t *V_pages, const ksa_pages *pages,
+                                const int32_t *cu_q, const int32_t *seq_lens, int32_t mask,
+                                float scale, uint16_t *out, float *lse, void *ws,
+                                size_t ws_bytes, uint32_t *dev_status, void *stream) {
+  return chunk_common(shape, num_tokens, q, q_stride, K_pages, V_pages, pages, true, cu_q,
+                      seq_lens, mask, scale, out, lse, ws, ws_bytes, dev_status, stream);
+}
+
 ksa_status ksa_get_device_status(const uint32_t *dev_status, void *stream, int32_t clear,
                                  uint32_t *flags) {
   if (dev_status == nullptr || flags == nullptr)

@@ -127,6 +127,63 @@ cudaError_t launch_gather_head_lists(const int32_t *lists, const int32_t *counts
                                      const int32_t *head, int B, int Hq, int k,
                                      int32_t *token_idx, int32_t *num_sel, cudaStream_t stream);
 
+// Page assignment and release (pages.cu): block tables and slots from lengths.
+struct AssignArgs {
+  const int32_t *ctx_lens, *new_lens;  // [B]
+  int32_t *block_table;                // [B, max_blocks]
+  const int32_t *free_pages;           // [num_pages], the stack
+  const int32_t *num_free;
+  int32_t *num_free_out;  // may be num_free
+  int32_t *seq_lens;      // [B], may be ctx_lens
+  int32_t *cu_new;        // [B + 1]
+  int64_t *slots;         // [N]
+  int32_t *positions;     // [N]
+  uint32_t *counter;      // workspace: zero between calls
+  uint32_t *status;
+  int B, T, bs, max_blocks, num_pages, N;
+};
+cudaError_t launch_assign_pages(const AssignArgs &a, cudaStream_t stream);
+struct ReleaseArgs {
+  const int32_t *done;  // [B]
+  int32_t *seq_lens, *block_table, *free_pages, *num_free;
+  uint32_t *counter, *status;
+  int B, T, bs, max_blocks, num_pages;
+};
+cudaError_t launch_release_pages(const ReleaseArgs &a, int num_sms, cudaStream_t stream);
+
+// Rotary positions and the cache write of N tokens (rotary.cu).
+struct RotaryArgs {
+  const uint16_t *q, *k, *v;  // token strides below; q null: no queries, k null: no cache write
+  uint16_t *q_out, *K, *V;
+  const int32_t *positions;  // [axes, N]
+  const int64_t *slots;      // [N]; null: every token is real and nothing goes to a cache
+  uint32_t *status;
+  long long q_stride, k_stride, v_stride, q_out_stride;
+  long long num_slots;  // < 2^31
+  int slots_per_page;   // T (contiguous cache) or bs
+  int N, Hq, Hkv, D, rotary_dim, interleaved;
+  double turns_per_step[64];  // inv_freq / 2 pi of each pair
+  uint8_t axis[64];
+};
+cudaError_t launch_rotary_append(const RotaryArgs &a, int num_sms, cudaStream_t stream);
+
+// Attention of ragged query chunks over the cache (chunk_attn.cu).
+struct ChunkArgs {
+  const uint16_t *q, *K, *V;
+  const int32_t *cu_q;      // [B + 1]
+  const int32_t *seq_lens;  // [B]
+  uint16_t *out;            // [N, Hq, D]
+  float *lse;               // [N, Hq] or null
+  uint32_t *status;
+  long long q_stride;
+  int B, Hq, Hkv, D, T, N;
+  int causal;
+  float scale;
+  KvLayout kv;
+};
+size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int N, int num_sms);
+cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStream_t stream);
+
 // Resident CTAs per SM of `func` launched with `threads` threads and `smem`
 // bytes of dynamic shared memory, on the current device.  The first query per
 // (device, kernel, threads, smem) raises the kernel's dynamic shared-memory

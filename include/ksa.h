@@ -12,10 +12,11 @@
  *
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers, dense row-major, owned by the
- *     caller; the one exception, head_of_row of ksa_select_tokens_one_head, is
- *     a host array.  The library allocates nothing, keeps no state between calls,
- *     and never synchronises the host: work is enqueued on `stream`
- *     (a cudaStream_t passed as void*; NULL = the legacy default stream).
+ *     caller; the exceptions, head_of_row of ksa_select_tokens_one_head and the
+ *     tables of ksa_rotary, are host arrays.  The library allocates nothing,
+ *     keeps no state between calls, and never synchronises the host: work is
+ *     enqueued on `stream` (a cudaStream_t passed as void*; NULL = the legacy
+ *     default stream).
  *   - bf16 tensors are passed as uint16_t* (the raw bf16 bit patterns).
  *   - Shapes: B = batch, Hq / Hkv = query / kv heads (G = Hq/Hkv query heads
  *     share one kv-head), D = head_dim, T = capacity (tokens per cache row),
@@ -79,7 +80,8 @@ enum {
   KSA_FLAG_SEQ_LEN_CLAMPED = 1u << 0, /* some seq_len was outside [1, T] */
   KSA_FLAG_INDEX_SKIPPED = 1u << 1,   /* some index entry named no valid token */
   KSA_FLAG_NONFINITE_SCORE = 1u << 2, /* a NaN score was ranked lowest */
-  KSA_FLAG_WAIT_TIMEOUT = 1u << 3     /* a pipeline wait gave up: results invalid */
+  KSA_FLAG_WAIT_TIMEOUT = 1u << 3,    /* a pipeline wait gave up: results invalid */
+  KSA_FLAG_NO_PAGE = 1u << 4          /* the stack of free pages ran out, or over */
 };
 
 /*
@@ -392,6 +394,170 @@ ksa_status ksa_sparse_decode_attn_noalloc(const ksa_shape *shape, const uint16_t
                                           int32_t tokens_per_idx, int32_t idx_shared,
                                           float scale, int32_t out_dtype, void *out,
                                           float *lse, uint32_t *dev_status, void *stream);
+
+/*
+ * Page assignment: block tables and token slots of a paged cache from request
+ * lengths, on the device, so that a serving step needs no host round trip
+ * between its scheduler's lengths and its kernels.
+ * Row b holds c_b = ctx_lens[b] tokens and takes n_b = new_lens[b] more,
+ * L_b = c_b + n_b.  It owns the pages of its first ceil(c_b / bs) blocks and
+ * takes one page for each block up to ceil(L_b / bs).  Free pages are a stack:
+ * free_pages[0, F), F = num_free[0].  With the rows in order, and each row's
+ * blocks in order, the k-th page taken is free_pages[F-1-k].  The new tokens
+ * of all rows lie one row after another on one axis of num_tokens places:
+ *   cu_new[b]    = n_0 + ... + n_{b-1}, cu_new[B] their total
+ *   positions[t] = c_b + t - cu_new[b]          (t in row b's part)
+ *   slots[t]     = page * bs + positions[t] % bs, page = the block's
+ *   seq_lens[b]  = L_b,   num_free_out[0] = F - pages taken
+ * Places behind the last row's tokens get slot and position -1 (padding).
+ * A row that cannot be served is refused whole: it takes no page, its
+ * seq_lens is c_b, and its tokens' slots and positions are -1.  That is a row
+ *   - whose pages, with those of all rows before it, exceed F
+ *     (KSA_FLAG_NO_PAGE; a row that needs no page is still served), or
+ *   - with c_b or n_b outside [0, T] (clamped there), L_b > T, or tokens past
+ *     num_tokens (KSA_FLAG_SEQ_LEN_CLAMPED).
+ * A page id outside [0, num_pages), in the table or on the stack, is never
+ * used: its tokens get slot -1, its table entry -1 (KSA_FLAG_INDEX_SKIPPED).
+ *   ctx_lens, new_lens: [B] int32;  num_free: [1] int32 (read; F outside
+ *                [0, num_pages] is clamped and flagged KSA_FLAG_NO_PAGE)
+ *   block_table: [B, max_blocks] int32 (entries of the new blocks written, no
+ *                others), T = shape->capacity = max_blocks * block_size
+ *   free_pages:  [num_pages] int32 (read)
+ *   num_free_out [1], seq_lens [B], cu_new [B+1] int32, slots [num_tokens]
+ *                int64, positions [num_tokens] int32 (written)
+ *   ws:          256 bytes, 256-byte aligned, zero-filled once (see
+ *                "Workspaces"); both page calls may share it
+ * seq_lens may be ctx_lens and num_free_out may be num_free (a loop that
+ * carries its lengths in place); no other overlap.  num_tokens may be 0
+ * (slots and positions are then not used).  Only batch, capacity and
+ * block_size of the shape matter.  One launch.
+ */
+ksa_status ksa_assign_pages(const ksa_shape *shape, const int32_t *ctx_lens,
+                            const int32_t *new_lens, int32_t *block_table, int32_t max_blocks,
+                            int32_t num_pages, const int32_t *free_pages,
+                            const int32_t *num_free, int32_t *num_free_out,
+                            int32_t num_tokens, int32_t *seq_lens, int32_t *cu_new,
+                            int64_t *slots, int32_t *positions, void *ws, size_t ws_bytes,
+                            uint32_t *dev_status, void *stream);
+
+/*
+ * The inverse: every row with done[b] != 0 gives its pages back.  The pages of
+ * its blocks j < ceil(seq_lens[b] / bs) go onto the stack, the last such row's
+ * last block first (releasing what one ksa_assign_pages call took for rows
+ * that held nothing leaves the stack as it was, bit for bit), its table
+ * entries become -1 and its seq_lens 0 (so a second release does nothing).
+ * Other rows are untouched.  A table entry that names no page is pushed as -1,
+ * where a later assignment flags it, and pages past the stack's num_pages
+ * places are dropped (KSA_FLAG_INDEX_SKIPPED, KSA_FLAG_NO_PAGE).
+ *   done: [B] int32 (read);  seq_lens [B], block_table, free_pages
+ *   [num_pages], num_free [1]: read and written.  ws: as above.  One launch.
+ */
+ksa_status ksa_release_pages(const ksa_shape *shape, const int32_t *done, int32_t *seq_lens,
+                             int32_t *block_table, int32_t max_blocks, int32_t num_pages,
+                             int32_t *free_pages, int32_t *num_free, void *ws,
+                             size_t ws_bytes, uint32_t *dev_status, void *stream);
+
+/*
+ * Rotary positions with one or more axes (time; or time, height and width of
+ * images and video), and the write of the rotated keys and the values into the
+ * cache: the step between the q/k/v projections and attention.  The leading
+ * rotary_dim = 2P dims of a head are P pairs; pair i turns by the angle
+ *   a(n, i) = positions[axis_of_pair[i], n] * inv_freq[i]:
+ *   (x, y) -> (x cos a - y sin a, x sin a + y cos a)
+ * where the pair is dims (i, i + P), or (2i, 2i + 1) when interleaved.  The
+ * other dims pass unchanged.  The angle is reduced to one turn in fp64, so
+ * far positions lose nothing; sine, cosine and products are fp32, rounded once
+ * to bf16.
+ */
+typedef struct {
+  int32_t rotary_dim;          /* 2P: a multiple of 16, 16 <= rotary_dim <= D */
+  int32_t num_axes;            /* rows of positions, 1 <= num_axes <= 8 */
+  int32_t interleaved;         /* 0: pairs (i, i + P); 1: pairs (2i, 2i + 1) */
+  const double *inv_freq;      /* [P] HOST array, finite */
+  const int32_t *axis_of_pair; /* [P] HOST array in [0, num_axes), or NULL: all 0 */
+} ksa_rotary;
+
+/*
+ * For every token n < num_tokens with slot s = slots[n] >= 0:
+ *   q_out[n, h, :] = rotated q[n, h, :],
+ *   K[b, g, t, :]  = rotated k[n, g, :],  V[b, g, t, :] = v[n, g, :],
+ * slot s = b * T + t in a contiguous cache, s = page * bs + offset in a paged
+ * one (the slots of ksa_assign_pages).  A negative slot is padding: nothing of
+ * the token is read or written.  A slot past the cache likewise, and it sets
+ * KSA_FLAG_INDEX_SKIPPED.  Slots must be distinct.
+ *   rotary:    read before the call returns; NULL: K/V are written unrotated
+ *              (encoder states), q must then be NULL
+ *   q, q_out:  bf16, token strides q_stride and q_out_stride elements, heads
+ *              and dims dense (e.g. columns of a fused projection); both NULL:
+ *              no queries.  q_out may be q with the same stride.
+ *   k, v:      bf16, token strides k_stride, v_stride; k, v, K, V all NULL: no
+ *              cache write, and slots may be NULL (every token is real)
+ *   positions: [num_axes, num_tokens] int32 (any value; not used if rotary is
+ *              NULL);  slots: [num_tokens] int64
+ * Pointers 16-byte aligned and strides multiples of 8, else
+ * KSA_ERR_INVALID_ARG.  num_tokens = 0 does nothing.  The contiguous form
+ * does not use block_size.  One launch, no workspace.
+ */
+ksa_status ksa_rotary_append_kv(const ksa_shape *shape, int32_t num_tokens,
+                                const ksa_rotary *rotary, const uint16_t *q, int32_t q_stride,
+                                const uint16_t *k, int32_t k_stride, const uint16_t *v,
+                                int32_t v_stride, const int32_t *positions,
+                                const int64_t *slots, uint16_t *q_out, int32_t q_out_stride,
+                                uint16_t *K, uint16_t *V, uint32_t *dev_status, void *stream);
+/* ksa_rotary_append_kv into page pools [num_pages, Hkv, bs, D]; the slots name
+ * the pages, so no block table is read.  Only heads, head_dim and block_size
+ * of the shape matter. */
+ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens,
+                                      const ksa_rotary *rotary, const uint16_t *q,
+                                      int32_t q_stride, const uint16_t *k, int32_t k_stride,
+                                      const uint16_t *v, int32_t v_stride,
+                                      const int32_t *positions, const int64_t *slots,
+                                      uint16_t *q_out, int32_t q_out_stride,
+                                      uint16_t *K_pages, uint16_t *V_pages, int32_t num_pages,
+                                      uint32_t *dev_status, void *stream);
+
+/*
+ * Attention of several query tokens per row over the cache: a decoder's tokens
+ * over an encoder's states of another length (KSA_MASK_NONE), or a chunk of a
+ * prompt, or drafted tokens to verify, over the row's own history with the
+ * chunk as its newest tokens (KSA_MASK_CAUSAL).  Row b has the queries n in
+ * [cu_q[b], cu_q[b+1]) and L_b = seq_lens[b] cached tokens; for query i of its
+ * N_b, head h (kv-head g = h / G):
+ *   visible t:  t < L_b, and t <= L_b - N_b + i when causal
+ *   z_t = scale * <q[n,h,:], K[b,g,t,:]>,  w = softmax(z over the visible t),
+ *   out[n,h,:] = sum_t w_t V[b,g,t,:],  lse[n,h] = log sum_t exp(z_t).
+ * A query that sees nothing (L_b = 0, or more new tokens than cached ones)
+ * gives out = 0 and lse = -inf.  What the cache holds outside the visible
+ * tokens (NaN, infinities) does not matter.  Scores, the running maximum and
+ * sum and the output accumulate in fp32; the weights are rounded to bf16 for
+ * the product with V (relative error up to 2^-8 each), and out once to bf16.
+ *   q:    bf16, token stride q_stride elements (a multiple of 8), heads and
+ *         dims dense;  cu_q: [B+1] int32, ascending;  seq_lens: [B] int32
+ *         (0 is allowed; outside [0, T] is clamped and flagged)
+ *   out:  [num_tokens, Hq, D] bf16 dense;  lse: [num_tokens, Hq] fp32, nullable
+ *   ws:   ksa_chunk_attn_workspace() bytes, 256-byte aligned, zero-filled once
+ *         (see "Workspaces")
+ * scale == 0 selects 1/sqrt(D).  Places of q and out that no row covers are
+ * left alone.  Entries of cu_q outside [0, num_tokens] or descending are
+ * clamped and flagged KSA_FLAG_SEQ_LEN_CLAMPED; num_tokens = 0 does nothing.
+ * Limits: D in {64, 128}; G <= 128.
+ */
+enum { KSA_MASK_NONE = 0, KSA_MASK_CAUSAL = 1 };
+size_t ksa_chunk_attn_workspace(const ksa_shape *shape, int32_t num_tokens);
+ksa_status ksa_chunk_attn(const ksa_shape *shape, int32_t num_tokens, const uint16_t *q,
+                          int32_t q_stride, const uint16_t *K, const uint16_t *V,
+                          const int32_t *cu_q, const int32_t *seq_lens, int32_t mask,
+                          float scale, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
+                          uint32_t *dev_status, void *stream);
+/* ksa_chunk_attn on a paged cache (see "Paged KV cache"): pages of block_size
+ * 16, 32 or 64 tokens; the tokens of a page id outside the pool are not
+ * visible and set KSA_FLAG_INDEX_SKIPPED. */
+ksa_status ksa_chunk_attn_paged(const ksa_shape *shape, int32_t num_tokens, const uint16_t *q,
+                                int32_t q_stride, const uint16_t *K_pages,
+                                const uint16_t *V_pages, const ksa_pages *pages,
+                                const int32_t *cu_q, const int32_t *seq_lens, int32_t mask,
+                                float scale, uint16_t *out, float *lse, void *ws,
+                                size_t ws_bytes, uint32_t *dev_status, void *stream);
 
 /*
  * LessIsMore unified selection [LIM s.2, s.5 "token selection layer"].

@@ -363,3 +363,120 @@ def test_validation_of_the_decode_step_and_append(ksa):
     odd = ctypes.c_void_p(0x1008)  # 8-byte aligned only
     assert lib.ksa_append_kv(ctypes.byref(sh), odd, FAKE, FAKE, FAKE, FAKE, None, None) == 1
     assert "aligned" in ksa.ksa_last_error()
+
+
+def test_validation_of_page_assignment_and_release(ksa):
+    lib = ksa.lib()
+    sh = _shape(ksa, B=2, T=64, bs=16)
+    BIG = 1 << 20
+
+    def assign(**kw):
+        a = dict(sh=sh, ctx=FAKE, new=FAKE, table=FAKE, mb=4, pages=9, free=FAKE, nf=FAKE,
+                 nfo=FAKE, n=5, seq=FAKE, cu=FAKE, slots=FAKE, pos=FAKE, ws=FAKE, wsb=BIG)
+        a.update(kw)
+        return lib.ksa_assign_pages(ctypes.byref(a["sh"]), a["ctx"], a["new"], a["table"],
+                                    a["mb"], a["pages"], a["free"], a["nf"], a["nfo"], a["n"],
+                                    a["seq"], a["cu"], a["slots"], a["pos"], a["ws"], a["wsb"],
+                                    None, None)
+
+    for kw in (dict(ctx=None), dict(new=None), dict(table=None), dict(free=None), dict(nf=None),
+               dict(nfo=None), dict(seq=None), dict(cu=None), dict(slots=None), dict(pos=None),
+               dict(mb=0), dict(mb=3), dict(pages=0), dict(n=-1), dict(n=1 << 30),
+               dict(slots=ctypes.c_void_p(0x1004)), dict(ctx=ctypes.c_void_p(0x1002))):
+        assert assign(**kw) == 1, kw
+        assert ksa.ksa_last_error() != ""
+    assert assign(sh=_shape(ksa, bs=8)) == 2
+    for kw in (dict(ws=None), dict(wsb=255), dict(ws=ctypes.c_void_p(0x1010))):
+        assert assign(**kw) == 3, kw
+
+    def release(**kw):
+        a = dict(done=FAKE, seq=FAKE, table=FAKE, mb=4, pages=9, free=FAKE, nf=FAKE, ws=FAKE)
+        a.update(kw)
+        return lib.ksa_release_pages(ctypes.byref(sh), a["done"], a["seq"], a["table"], a["mb"],
+                                     a["pages"], a["free"], a["nf"], a["ws"], BIG, None, None)
+
+    for kw in (dict(done=None), dict(seq=None), dict(table=None), dict(mb=5), dict(pages=0),
+               dict(free=None), dict(nf=None)):
+        assert release(**kw) == 1, kw
+    assert release(ws=None) == 3
+
+
+def test_validation_of_rotary_appends(ksa):
+    """The rotation's tables are checked entry by entry on the host; pointers come in groups;
+    strides hold the heads and keep 16-byte chunks."""
+    lib = ksa.lib()
+    sh = _shape(ksa, B=1, Hq=4, Hkv=2, D=128, T=64, bs=16)
+    good = ksa.Rotary([0.5] * 64)
+
+    def call(rot=good, paged=False, **kw):
+        a = dict(sh=sh, n=3, q=FAKE, qs=512, k=FAKE, ks=256, v=FAKE, vs=256, pos=FAKE, slots=FAKE,
+                 qo=FAKE, qos=512, K=FAKE, V=FAKE, pages=4)
+        a.update(kw)
+        args = [ctypes.byref(a["sh"]), a["n"], rot._ref if rot is not None else None, a["q"],
+                a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["pos"], a["slots"], a["qo"],
+                a["qos"], a["K"], a["V"]]
+        if paged:
+            return lib.ksa_rotary_append_kv_paged(*args, a["pages"], None, None)
+        return lib.ksa_rotary_append_kv(*args, None, None)
+
+    odd = ctypes.c_void_p(0x1008)
+    for kw in (dict(n=-1), dict(q=None), dict(qo=None), dict(k=None), dict(v=None), dict(K=None),
+               dict(V=None), dict(slots=None), dict(pos=None), dict(q=odd), dict(K=odd),
+               dict(qs=511), dict(qs=516), dict(qs=504), dict(ks=248), dict(vs=250), dict(qos=8),
+               dict(rot=None), dict(qos=520),
+               dict(q=None, qo=None, k=None, v=None, K=None, V=None),
+               dict(rot=ksa.Rotary([0.5] * 4)), dict(rot=ksa.Rotary([0.5] * 9)),
+               dict(rot=ksa.Rotary([0.5] * 72)), dict(rot=ksa.Rotary([])),
+               dict(rot=ksa.Rotary([0.5] * 63 + [float("inf")])),
+               dict(rot=ksa.Rotary([float("nan")] * 64)),
+               dict(rot=ksa.Rotary([0.5] * 64, [0] * 63 + [2], num_axes=2)),
+               dict(rot=ksa.Rotary([0.5] * 64, [-1] + [0] * 63, num_axes=2)),
+               dict(rot=ksa.Rotary([0.5] * 64, num_axes=9)),
+               dict(paged=True, pages=0)):
+        assert call(**kw) == 1, kw
+        assert ksa.ksa_last_error() != ""
+    assert call(paged=True, pages=1 << 27) == 2
+    assert call(paged=True, sh=_shape(ksa, bs=8)) == 2
+    assert call(sh=_shape(ksa, D=96)) == 2
+    assert call(n=0, q=None) == 0  # nothing to do
+    with pytest.raises(ValueError):
+        ksa.Rotary([0.5] * 64, [0] * 3)
+
+
+def test_validation_of_chunk_attention(ksa):
+    lib = ksa.lib()
+    sh = _shape(ksa, B=2, Hq=4, Hkv=2, D=128, T=64, bs=16)
+    need = lib.ksa_chunk_attn_workspace(ctypes.byref(sh), 7)
+    assert need >= 256 and need % 256 == 0
+    pages = ksa.Pages(FAKE, 4, 10)
+
+    def call(paged=False, **kw):
+        a = dict(sh=sh, n=7, q=FAKE, qs=512, K=FAKE, V=FAKE, cu=FAKE, seq=FAKE, mask=1, scale=0.0,
+                 out=FAKE, lse=None, ws=FAKE, wsb=need, pages=ctypes.byref(pages))
+        a.update(kw)
+        rest = [a["cu"], a["seq"], a["mask"], a["scale"], a["out"], a["lse"], a["ws"], a["wsb"],
+                None, None]
+        args = [ctypes.byref(a["sh"]), a["n"], a["q"], a["qs"], a["K"], a["V"]]
+        if paged:
+            return lib.ksa_chunk_attn_paged(*args, a["pages"], *rest)
+        return lib.ksa_chunk_attn(*args, *rest)
+
+    odd = ctypes.c_void_p(0x1008)
+    for kw in (dict(n=-1), dict(q=None), dict(K=None), dict(V=None), dict(cu=None), dict(seq=None),
+               dict(out=None), dict(q=odd), dict(V=odd), dict(out=odd), dict(mask=2),
+               dict(mask=-1), dict(scale=-1.0), dict(scale=float("inf")),
+               dict(scale=float("nan")), dict(qs=504), dict(qs=516),
+               dict(lse=ctypes.c_void_p(0x1002)), dict(paged=True, pages=None),
+               dict(paged=True, pages=ctypes.byref(ksa.Pages(FAKE, 3, 10))),
+               dict(paged=True, pages=ctypes.byref(ksa.Pages(FAKE, 4, 0)))):
+        assert call(**kw) == 1, kw
+        assert ksa.ksa_last_error() != ""
+    for kw in (dict(ws=None), dict(wsb=need - 1), dict(ws=ctypes.c_void_p(0x1010))):
+        assert call(**kw) == 3, kw
+    assert call(sh=_shape(ksa, Hq=258, Hkv=2)) == 2
+    assert call(sh=_shape(ksa, D=96)) == 2
+    assert call(paged=True, sh=_shape(ksa, bs=8)) == 2
+    assert call(n=1 << 30) == 2
+    assert call(n=0, q=None) == 0
+    bad = _shape(ksa, D=96)
+    assert lib.ksa_chunk_attn_workspace(ctypes.byref(bad), 7) == 0

@@ -1,0 +1,710 @@
+"""Page assignment, rotary cache writes and chunk attention against plain 64-bit forms.
+
+Whole numbers must be equal.  A bf16 value is off by at most half a step, 2^-8 of it, besides
+the fp32 arithmetic before the rounding:
+  rotary     sine and cosine within 1e-6 (fp32 turns and sincospi), products and sum 3 * 2^-24:
+             2^-8 |x| + 2e-6 (|a| + |b|)
+  attention  weights rounded to bf16 (2^-8 each), out rounded (2^-8), scores off by D 2^-24 of
+             their terms' absolute sum (below 1e-4 here, so a weight by 2e-4):
+             (2^-8 + 4e-4) sum w |v| + 2^-8 |out|;  lse 1e-4
+"""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+HALF = 2.0 ** -8
+
+
+@pytest.fixture(scope="module")
+def ksa():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import block_top_sparse_ksa_b200 as k
+    k.lib()
+    return k
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def randn(shape, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device=DEV).to(torch.bfloat16)
+
+
+# ---------------------------------------------------------------------------
+# pages
+
+
+def ref_assign(ctx, new, table, free, F, bs, N, T, num_pages):
+    """The definition, row by row, with Python integers."""
+    table, seq, slots, pos = table.copy(), [], [-1] * N, [-1] * N
+    cu, at, asked, taken = [0], 0, 0, 0
+    flags = 0
+    for b, (c0, n0) in enumerate(zip(ctx, new)):
+        c, n = min(max(c0, 0), T), min(max(n0, 0), T)
+        bad = c != c0 or n != n0 or c + n > T or (n > 0 and at + n > N)
+        held = -(-c // bs)
+        need = 0 if bad else -(-(c + n) // bs) - held
+        none = need > 0 and asked + need > F
+        if bad:
+            flags |= 1
+        if none:
+            flags |= 16
+        if not bad and not none:
+            for i in range(need):
+                p = free[F - 1 - (asked + i)]
+                if not 0 <= p < num_pages:
+                    p = -1
+                    flags |= 2
+                table[b, held + i] = p
+            taken += need
+            for i in range(n):
+                p = table[b, (c + i) // bs]
+                pos[at + i] = c + i
+                if 0 <= p < num_pages:
+                    slots[at + i] = int(p) * bs + (c + i) % bs
+                else:
+                    flags |= 2
+        seq.append(c if bad or none else c + n)
+        asked += need
+        at += n
+        cu.append(min(at, N))
+    return table, F - taken, seq, cu, slots, pos, flags
+
+
+def page_state(rng, ctx, mb, bs, spare):
+    """Tables of the held blocks and the stack of the other pages, in random order."""
+    held = [min(mb, max(0, -(-c // bs))) for c in ctx]
+    pool = sum(held) + spare
+    perm = rng.permutation(pool).astype(np.int32)
+    table = np.full((len(ctx), mb), -1, np.int32)
+    k = 0
+    for b, h in enumerate(held):
+        table[b, :h] = perm[k:k + h]
+        k += h
+    free = np.full(pool, -1, np.int32)
+    free[:spare] = perm[k:]
+    return table, free, spare, pool
+
+
+def run_assign(ksa, ctx, new, table, free, F, bs, N, **kw):
+    st = status()
+    t, nf, out = torch.from_numpy(table).to(DEV), i32([F]), torch.full((1,), -7).to(DEV).int()
+    seq, cu, slots, pos = ksa.ksa_assign_pages(i32(ctx), i32(new), t, torch.from_numpy(free).to(DEV),
+                                               nf, bs, N, num_free_out=out, dev_status=st, **kw)
+    assert int(nf) == F
+    return t, out, seq, cu, slots, pos, int(st)
+
+
+def same_assign(got, want):
+    t, out, seq, cu, slots, pos, flags = got
+    np.testing.assert_array_equal(t.cpu().numpy(), want[0])
+    assert int(out) == want[1]
+    assert seq.tolist() == want[2] and cu.tolist() == want[3]
+    assert slots.dtype == torch.int64 and slots.tolist() == want[4]
+    assert pos.tolist() == want[5]
+    assert flags == want[6]
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64])
+@pytest.mark.parametrize("B,new,tail", [(1, 1, 0), (1, 4000, 5), (7, 1, 0), (33, 100, 3),
+                                        (1023, 2, 0), (1025, 1, 9), (2500, 3, 0), (300, 40, 1)])
+def test_assign_pages(ksa, bs, B, new, tail):
+    rng = np.random.default_rng(B * 100 + new + bs)
+    mb = 4096 // bs + new // bs + 2
+    ctx = rng.integers(0, 4096, B).tolist()
+    ctx[0] = [0, bs, 2 * bs - 1][bs // 32]
+    n = (rng.integers(0, new + 1, B) if new > 1 else np.ones(B, int)).tolist()
+    need = sum(-(-(c + k) // bs) - -(-c // bs) for c, k in zip(ctx, n))
+    table, free, F, pool = page_state(rng, ctx, mb, bs, need + 3)
+    N = sum(n) + tail
+    want = ref_assign(ctx, n, table, free, F, bs, N, mb * bs, pool)
+    same_assign(run_assign(ksa, ctx, n, table, free, F, bs, N), want)
+
+
+def test_assign_pages_refuses_whole_rows(ksa):
+    """Out of pages, past the table, past the token axis, negative lengths: the row is refused
+    whole and flagged, rows that need no page are still served."""
+    bs, mb = 16, 8
+    rng = np.random.default_rng(5)
+    T = mb * bs
+    cases = [
+        ([0, 16, 3, 0, 5], [40, 16, 2, 1, 0], 4, 59),      # the stack runs out at row 3
+        ([0, 16, 3, 0, 5], [40, 16, 2, 1, 0], 0, 59),      # an empty stack
+        ([0, 120, 128, 129], [128, 9, 0, 1], 30, 200),     # L > T, c > T
+        ([-1, 4, 4], [3, -2, 3], 10, 20),                  # negative lengths
+        ([0, 0, 0], [10, 10, 10], 10, 25),                 # row 2 passes the token axis
+        ([0, 0], [0, 0], 3, 0),                            # nothing new, no token axis
+        ([0], [2 ** 31 - 1], 3, 7),
+    ]
+    for ctx, new, spare, N in cases:
+        table, free, F, pool = page_state(rng, ctx, mb, bs, spare)
+        if not pool:
+            continue
+        want = ref_assign(ctx, new, table, free, F, bs, N, T, pool)
+        same_assign(run_assign(ksa, ctx, new, table, free, F, bs, N), want)
+
+
+def test_assign_pages_skips_bad_page_ids(ksa):
+    bs, mb = 16, 6
+    table = np.full((2, mb), -1, np.int32)
+    table[0, 0], table[1, 0] = 99, 1  # row 0's held block names no page
+    free = np.array([0, 2, -5, 3, 77, 4], np.int32)
+    ctx, new = [5, 16], [40, 33]
+    want = ref_assign(ctx, new, table, free, 6, bs, 80, mb * bs, 6)
+    got = run_assign(ksa, ctx, new, table, free, 6, bs, 80)
+    same_assign(got, want)
+    assert got[-1] == 2
+    # a count outside the stack is clamped and flagged
+    got = run_assign(ksa, [0], [16], table[:1], free, 9, bs, 16)
+    assert got[-1] & 16 and got[0][0, 0] == 4 and int(got[1]) == 5
+
+
+def test_assign_in_place_steps_in_a_graph(ksa):
+    """The decode loop's form: lengths and count carried in place, captured once, replayed; 40
+    steps over two pages per row, many CTAs."""
+    B, bs, mb = 3000, 16, 6
+    rng = np.random.default_rng(3)
+    ctx0 = rng.integers(0, 40, B).astype(np.int32)
+    table0, free0, F, pool = page_state(rng, ctx0.tolist(), mb, bs, 3 * B)
+    lens, table = torch.from_numpy(ctx0).to(DEV), torch.from_numpy(table0).to(DEV)
+    free, count = torch.from_numpy(free0).to(DEV), i32([F])
+    one = torch.ones(B, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    cu, slots, pos = (torch.zeros(k, dtype=d, device=DEV) for k, d in
+                      ((B + 1, torch.int32), (B, torch.int64), (B, torch.int32)))
+
+    def step():
+        ksa.ksa_assign_pages(lens, one, table, free, count, bs, B, seq_lens=lens, cu_new=cu,
+                             slots=slots, positions=pos, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(38):
+        graph.replay()
+    torch.cuda.synchronize()
+    c, f, t = ctx0.tolist(), F, table0
+    for _ in range(39):
+        t, f, c, _, sl, ps, flags = ref_assign(c, [1] * B, t, free0, f, bs, B, mb * bs, pool)
+        assert flags == 0
+    assert lens.tolist() == c and int(count) == f
+    np.testing.assert_array_equal(table.cpu().numpy(), t)
+    assert slots.tolist() == sl and pos.tolist() == ps
+    assert int(ws[:4].view(torch.int32)) == 0
+    del graph
+
+
+@pytest.mark.parametrize("B", [1, 5, 1024, 1025, 3000])
+def test_release_undoes_assign(ksa, B):
+    bs, mb = 16, 9
+    rng = np.random.default_rng(B)
+    new = rng.integers(0, mb * bs + 1, B).tolist()
+    table, free, F, pool = page_state(rng, [0] * B, mb, bs, sum(-(-n // bs) for n in new) + 4)
+    t, count = torch.from_numpy(table).to(DEV), i32([F])
+    stack = torch.from_numpy(free).to(DEV)
+    seq, *_ = ksa.ksa_assign_pages(i32([0] * B), i32(new), t, stack, count, bs, sum(new))
+    assert int(count) == 4
+    # some rows first, the others after; then nothing is left to give
+    first = torch.from_numpy(rng.integers(0, 2, B).astype(np.int32)).to(DEV)
+    t1 = t.clone()
+    ksa.ksa_release_pages(seq, first, t, stack, count, bs)
+    gone = [r for r in range(B) if first[r]]
+    want = [int(p) for r in reversed(gone) for p in t1[r, :-(-new[r] // bs)].flip(0).tolist()]
+    assert stack[4:int(count)].tolist() == want
+    assert all((t[r] == -1).all() for r in gone) and all(seq[r] == 0 for r in gone)
+    keep = [r for r in range(B) if not first[r]]
+    assert torch.equal(t[keep], t1[keep])
+    assert sorted(stack[:int(count)].tolist()) == sorted(set(stack[:int(count)].tolist()))
+    ksa.ksa_release_pages(seq, torch.ones_like(first), t, stack, count, bs)
+    assert int(count) == F and int(seq.abs().sum()) == 0 and bool((t == -1).all())
+    assert sorted(stack[:F].tolist()) == sorted(free[:F].tolist())
+    before = stack.clone()
+    ksa.ksa_release_pages(seq, torch.ones_like(first), t, stack, count, bs)
+    assert int(count) == F and torch.equal(stack, before)
+    # all rows in one call: the stack as it was, bit for bit
+    t, stack = torch.from_numpy(table).to(DEV), torch.from_numpy(free).to(DEV)
+    seq, *_ = ksa.ksa_assign_pages(i32([0] * B), i32(new), t, stack, count, bs, sum(new))
+    ksa.ksa_release_pages(seq, torch.ones_like(first), t, stack, count, bs)
+    assert int(count) == F and torch.equal(stack.cpu(), torch.from_numpy(free))
+
+
+def test_release_flags_bad_entries_and_a_full_stack(ksa):
+    bs = 16
+    table = torch.tensor([[1, 9], [2, 3]], dtype=torch.int32, device=DEV)
+    stack, count, st = i32([0, -1, -1, -1]), i32([1]), status()
+    seq = i32([20, 40])  # row 1's length is past its table
+    ksa.ksa_release_pages(seq, i32([1, 1]), table, stack, count, bs, dev_status=st)
+    # pushed: 3, 2, bad, (1 dropped: four places)
+    assert stack.tolist() == [0, 3, 2, -1] and int(count) == 4
+    assert int(st) == (1 | 2 | 16) and bool((table == -1).all()) and seq.tolist() == [0, 0]
+
+
+# ---------------------------------------------------------------------------
+# rotary
+
+
+def ref_rotary(x, pos, axis, freq, inter):
+    """x [N, H, D] bf16 -> rotated in fp64, and |a| + |b| of each element's pair."""
+    P = len(freq)
+    y, mag = x.double().cpu().numpy().copy(), np.abs(x.double().cpu().numpy())
+    mag = mag.copy()
+    ang = pos.cpu().numpy().astype(np.longdouble)[axis].T * np.asarray(freq, np.longdouble)
+    c, s = np.cos(ang).astype(np.float64)[:, None], np.sin(ang).astype(np.float64)[:, None]
+    lo = slice(0, 2 * P, 2) if inter else slice(0, P)
+    hi = slice(1, 2 * P, 2) if inter else slice(P, 2 * P)
+    a, b = y[..., lo].copy(), y[..., hi].copy()
+    y[..., lo], y[..., hi] = a * c - b * s, a * s + b * c
+    mag[..., lo] = mag[..., hi] = np.abs(a) + np.abs(b)
+    return y, mag
+
+
+def close_rotary(got, want, mag, P):
+    g = got.double().cpu().numpy()
+    np.testing.assert_array_equal(g[..., 2 * P:], want[..., 2 * P:])  # behind the rotary dims
+    assert (np.abs(g - want) <= HALF * np.abs(want) + 2e-6 * mag).all()
+
+
+ROT = [  # N, Hq, Hkv, D, P, axes, interleaved, positions up to
+    (1, 4, 2, 128, 64, 1, False, 10), (3, 1, 1, 64, 32, 3, True, 100),
+    (70, 32, 8, 128, 64, 3, False, 1 << 20), (641, 5, 5, 64, 8, 2, True, 1 << 30),
+    (1000, 7, 1, 128, 24, 2, False, 50000), (2300, 16, 8, 128, 64, 8, True, 3000),
+    (593, 24, 8, 64, 16, 1, False, 2 ** 31 - 1), (592, 2, 1, 128, 56, 4, True, 1 << 24),
+]
+
+
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("N,Hq,Hkv,D,P,axes,inter,far", ROT)
+def test_rotary_append(ksa, paged, N, Hq, Hkv, D, P, axes, inter, far):
+    rng = np.random.default_rng(N + D + P)
+    qkv = randn((N, (Hq + 2 * Hkv) * D + 8), N)  # columns of a wider projection
+    q = qkv[:, :Hq * D].view(N, Hq, D)
+    k = qkv[:, Hq * D:(Hq + Hkv) * D].view(N, Hkv, D)
+    v = qkv[:, (Hq + Hkv) * D:(Hq + 2 * Hkv) * D].view(N, Hkv, D)
+    pos = torch.from_numpy(rng.integers(-far, far, (axes, N)).astype(np.int32)).to(DEV)
+    axis = [int(i) for i in rng.integers(0, axes, P)]
+    freq = [10000.0 ** (-i / P) for i in range(P)]
+    rot = ksa.Rotary(freq, axis, interleaved=inter, num_axes=axes)
+    bs, T = 16, 100
+    rows = -(-N // T) + 1
+    K = randn((N // bs + 4, Hkv, bs, D) if paged else (rows, Hkv, T, D), 7)
+    V = randn(tuple(K.shape), 8)
+    per = K.shape[2]
+    slots = rng.permutation(K.shape[0] * per)[:N].astype(np.int64)
+    slots[::5] = -1
+    if N > 2:
+        slots[2] = K.shape[0] * per  # past the cache
+    K0, V0 = K.clone(), V.clone()
+    q_out = torch.full((N, Hq, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    st = status()
+    call = ksa.ksa_rotary_append_kv_paged if paged else ksa.ksa_rotary_append_kv
+    call(q, k, v, pos, torch.from_numpy(slots).to(DEV), K, V, rot, q_out=q_out, dev_status=st)
+    assert int(st) == (2 if N > 2 else 0)
+    real = (slots >= 0) & (slots < K.shape[0] * per)
+    keep = torch.from_numpy(real).to(DEV)
+    want, mag = ref_rotary(q, pos, axis, freq, inter)
+    close_rotary(q_out[keep], want[real], mag[real], P)
+    assert bool((q_out[~keep] == 3.0).all())
+    pg, off = torch.from_numpy(slots[real] // per).to(DEV), torch.from_numpy(slots[real] % per).to(DEV)
+    want, mag = ref_rotary(k, pos, axis, freq, inter)
+    close_rotary(K[pg, :, off], want[real], mag[real], P)
+    assert torch.equal(V[pg, :, off], v[keep])
+    K0[pg, :, off], V0[pg, :, off] = K[pg, :, off], V[pg, :, off]
+    assert torch.equal(K, K0) and torch.equal(V, V0)  # the rest of the cache is untouched
+
+
+def test_rotary_parts(ksa):
+    """In place, queries only, keys and values only, no rotation, default axis; one stream other
+    than the current one."""
+    N, Hq, Hkv, D = 37, 8, 2, 128
+    q, k, v = randn((N, Hq, D), 1), randn((N, Hkv, D), 2), randn((N, Hkv, D), 3)
+    pos = torch.arange(N, dtype=torch.int32, device=DEV) + 1000
+    freq = [1e6 ** (-i / 64) for i in range(64)]
+    rot = ksa.Rotary(np.array(freq))
+    slots = torch.arange(N, device=DEV) + 5
+    K, V = (torch.zeros((1, Hkv, 64, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    out = ksa.ksa_rotary_append_kv(q, k, v, pos, slots, K, V, rot)
+    only = ksa.ksa_rotary_append_kv(q, None, None, pos, None, None, None, rot)
+    assert torch.equal(only, out)
+    K2, V2 = torch.zeros_like(K), torch.zeros_like(V)
+    assert ksa.ksa_rotary_append_kv(None, k, v, pos, slots, K2, V2, rot) is None
+    assert torch.equal(K2, K) and torch.equal(V2, V)
+    q2 = q.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ksa.ksa_rotary_append_kv(q2, None, None, pos[None], None, None, None, rot, q_out=q2,
+                             stream=side)
+    side.synchronize()
+    assert torch.equal(q2, out)
+    ksa.ksa_rotary_append_kv(None, k, v, None, slots, K2, V2, None)
+    assert torch.equal(K2[0, :, 5:5 + N], k.transpose(0, 1)) and torch.equal(V2, V)
+    empty = q[:0]
+    assert ksa.ksa_rotary_append_kv(empty, None, None, pos[None, :0], None, None, None,
+                                    rot).shape == (0, Hq, D)
+
+
+def test_rotary_offsets_past_32_bits(ksa):
+    """A pool of more than 2^31 elements: the last page's rows land where they belong."""
+    Hkv, bs, D = 8, 64, 128
+    P = (2 ** 31) // (Hkv * bs * D) + 3
+    K, V = (torch.empty((P, Hkv, bs, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k, v = randn((4, Hkv, D), 1), randn((4, Hkv, D), 2)
+    slots = torch.tensor([P * bs - 1, 0, (P - 2) * bs + 7, P * bs], device=DEV)
+    st = status()
+    ksa.ksa_rotary_append_kv_paged(None, k, v, None, slots, K, V, None, dev_status=st)
+    assert int(st) == 2
+    assert torch.equal(K[P - 1, :, bs - 1], k[0]) and torch.equal(V[P - 1, :, bs - 1], v[0])
+    assert torch.equal(K[0, :, 0], k[1]) and torch.equal(K[P - 2, :, 7], k[2])
+
+
+# ---------------------------------------------------------------------------
+# chunk attention
+
+
+def ref_attn(q, k, v, n, L, causal, scale):
+    """One row in fp64: q [n, Hq, D], k and v [Hkv, L, D] -> out, lse, sum w |v|."""
+    Hq, D = q.shape[1:]
+    G = Hq // k.shape[0]
+    k, v = k.double().repeat_interleave(G, 0), v.double().repeat_interleave(G, 0)
+    z = torch.einsum("nhd,htd->hnt", q.double(), k) * scale
+    if causal:
+        i, t = torch.arange(n, device=DEV)[:, None], torch.arange(L, device=DEV)
+        z = z.masked_fill(t > L - n + i, -torch.inf)
+    lse = torch.logsumexp(z, -1) if L else torch.full((Hq, n), -torch.inf, device=DEV).double()
+    w = torch.where(lse[..., None] == -torch.inf, 0.0, torch.exp(z - lse[..., None]))
+    return ((w @ v).transpose(0, 1), lse.T, (w @ v.abs()).transpose(0, 1))
+
+
+class Cache:
+    """Random K/V of the given row lengths, contiguous or paged, everything a row does not hold
+    poisoned with NaN and infinities."""
+
+    def __init__(self, lens, Hkv, D, bs, paged, seed, T=None, mean=0.0):
+        B = len(lens)
+        self.lens, self.paged = lens, paged
+        mb = max(1, -(-max(lens) // bs)) + 1
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        self.rows = [tuple((torch.randn((Hkv, L, D), generator=g, device=DEV) + mean)
+                           .to(torch.bfloat16) for _ in range(2)) for L in lens]
+        poison = [float("nan"), float("inf"), -float("inf")]
+        if paged:
+            need = sum(-(-L // bs) for L in lens)
+            P = need + 2
+            order = torch.randperm(P, generator=g, device=DEV).tolist()
+            self.K, self.V = (torch.empty((P, Hkv, bs, D), dtype=torch.bfloat16, device=DEV)
+                              for _ in range(2))
+            for x in (self.K, self.V):
+                for i, p in enumerate(poison):
+                    x[i::3] = p
+            table = np.full((B, mb), -1, np.int32)
+            for b, L in enumerate(lens):
+                for j in range(-(-L // bs)):
+                    p = order.pop()
+                    table[b, j] = p
+                    part = slice(j * bs, min(L, (j + 1) * bs))
+                    for x, src in zip((self.K, self.V), self.rows[b]):
+                        x[p, :, :part.stop - part.start] = src[:, part]
+            self.table = torch.from_numpy(table).to(DEV)
+        else:
+            T = T or max(1, max(lens)) + 3
+            self.K, self.V = (torch.empty((B, Hkv, T, D), dtype=torch.bfloat16, device=DEV)
+                              for _ in range(2))
+            for x, w in ((self.K, 0), (self.V, 1)):
+                for i, p in enumerate(poison):
+                    x[:, :, i::3] = p
+                for b, L in enumerate(lens):
+                    x[b, :, :L] = self.rows[b][w]
+
+    def call(self, ksa, q, cu, seq, mask, **kw):
+        if self.paged:
+            return ksa.ksa_chunk_attn_paged(q, self.K, self.V, self.table, cu, seq, mask, **kw)
+        return ksa.ksa_chunk_attn(q, self.K, self.V, cu, seq, mask, **kw)
+
+
+def check_attn(ksa, rows, Hq, Hkv, D, bs, paged, causal, seed, scale=0.0, mean=0.0, tail=0,
+               **kw):
+    """rows: (query tokens, cached tokens) of each row."""
+    nq, lens = [r[0] for r in rows], [r[1] for r in rows]
+    N = sum(nq) + tail
+    q = randn((max(N, 1), Hq, D), seed + 1)[:N]
+    cache = Cache(lens, Hkv, D, bs, paged, seed, mean=mean)
+    cu = i32(np.concatenate([[0], np.cumsum(nq)]))
+    out = torch.full((N, Hq, D), 5.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((N, Hq), 5.0, device=DEV)
+    st = status()
+    cache.call(ksa, q, cu, i32(lens), ksa.MASK_CAUSAL if causal else ksa.MASK_NONE, scale=scale,
+               out=out, lse=lse, dev_status=st, **kw)
+    assert int(st) == 0
+    at = 0
+    for b, (n, L) in enumerate(rows):
+        want, want_lse, mag = ref_attn(q[at:at + n], *cache.rows[b], n, L, causal,
+                                       scale or D ** -0.5)
+        got, got_lse = out[at:at + n].double(), lse[at:at + n].double()
+        bound = (HALF + 4e-4) * mag + HALF * want.abs()
+        off = ((got - want).abs() - bound).nan_to_num(nan=torch.inf)
+        assert bool((off <= 1e-30).all()), (b, n, L, float(off.max()))
+        empty = want_lse == -torch.inf
+        assert bool((got_lse[empty] == -torch.inf).all()) and bool((got[empty] == 0).all())
+        assert float((got_lse - want_lse)[~empty].abs().max().nan_to_num(nan=9.0)
+                     if (~empty).any() else 0.0) <= 1e-4, (b, n, L)
+        at += n
+    assert bool((out[at:] == 5.0).all()) and bool((lse[at:] == 5.0).all())
+    return cache, q, cu, out, lse
+
+
+EDGES = [(1, 1), (0, 5), (1, 0), (3, 127), (2, 128), (5, 129), (33, 33), (1, 300), (64, 255),
+         (31, 257), (7, 3), (0, 0), (130, 131), (1, 513), (260, 600)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,Hq,Hkv,bs,paged", [
+    (128, 8, 2, 16, True), (128, 4, 4, 32, False), (64, 8, 1, 64, True), (64, 6, 2, 16, False),
+    (128, 5, 1, 32, True), (128, 7, 1, 64, True), (64, 2, 2, 32, True), (128, 16, 2, 16, False),
+    (64, 40, 2, 16, True), (128, 130, 2, 16, True), (64, 128, 1, 64, False)])
+def test_chunk_attn_ragged(ksa, causal, D, Hq, Hkv, bs, paged):
+    check_attn(ksa, EDGES, Hq, Hkv, D, bs, paged, causal, seed=D + Hq + bs, tail=3)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("rows,Hq,Hkv,D,bs,paged", [
+    ([(1, 20000)], 4, 1, 128, 16, True),             # one token, a long axis
+    ([(5, 33001)], 32, 8, 128, 16, True),            # drafted tokens
+    ([(1, 5000), (1, 17), (1, 0), (1, 9001)], 8, 8, 64, 32, True),
+    ([(1, 4097)] * 32, 16, 8, 128, 16, False),       # a decode batch
+    ([(700, 700)], 8, 2, 128, 64, True),             # a prompt
+    ([(513, 5000), (1, 3000), (129, 129)], 4, 2, 64, 16, True),
+    ([(2049, 2049)], 2, 1, 128, 16, False),
+    ([(3, 70000)], 1, 1, 64, 64, False),
+])
+def test_chunk_attn_long(ksa, causal, rows, Hq, Hkv, D, bs, paged):
+    check_attn(ksa, rows, Hq, Hkv, D, bs, paged, causal, seed=len(rows) + Hq)
+
+
+@pytest.mark.parametrize("scale,mean", [(0.0, 1.0), (1.0, 0.0), (0.5, 2.0), (1e-3, 0.0)])
+def test_chunk_attn_scales(ksa, scale, mean):
+    """Peaked softmax (scale 1: weights of one token near 1) and flat ones; keys and values with
+    a mean, so that the running maximum moves by much."""
+    check_attn(ksa, [(40, 300), (200, 1000)], 4, 2, 64, 16, True, True, seed=3, scale=scale,
+               mean=mean)
+
+
+def test_chunk_attn_growing_scores(ksa):
+    """Scores that rise with every key tile by far more than a rescaling threshold, then fall."""
+    D, L, n = 64, 1500, 70
+    cache = Cache([L], 1, D, 16, False, 9)
+    ramp = torch.cat([torch.linspace(-6, 6, L // 2), torch.linspace(6, -6, L - L // 2)]).to(DEV)
+    k = cache.rows[0][0]
+    k[:] = ramp[None, :, None].to(torch.bfloat16)
+    cache.K[0, :, :L] = k
+    q = torch.ones((n, 2, D), dtype=torch.bfloat16, device=DEV)
+    cu, seq = i32([0, n]), i32([L])
+    lse = torch.empty((n, 2), device=DEV)
+    out, _ = cache.call(ksa, q, cu, seq, ksa.MASK_NONE, lse=lse)
+    want, want_lse, mag = ref_attn(q, k, cache.rows[0][1], n, L, False, D ** -0.5)
+    assert bool(((out.double() - want).abs() <= (HALF + 4e-4) * mag + HALF * want.abs()).all())
+    assert float((lse.double() - want_lse).abs().max()) <= 1e-4
+
+
+def test_chunk_attn_strided_q_streams_and_no_lse(ksa):
+    """q as columns of a projection, lse not asked for, a caller's workspace used by calls one
+    after another on another stream, results equal bit for bit."""
+    rows = [(9, 2000), (65, 700)]
+    cache, q, cu, out, lse = check_attn(ksa, rows, 4, 2, 128, 16, True, True, seed=21)
+    N = q.shape[0]
+    wide = torch.zeros((N, 4 * 128 + 256), dtype=torch.bfloat16, device=DEV)
+    wide[:, 64:64 + 512] = q.reshape(N, -1)
+    qs = wide[:, 64:64 + 512].view(N, 4, 128)
+    ws = torch.zeros(ksa.ksa_chunk_attn_workspace(2, 4, 2, 128, cache.table.shape[1] * 16, N),
+                     dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        got, none = cache.call(ksa, qs, cu, i32([2000, 700]), ksa.MASK_CAUSAL, workspace=ws,
+                               stream=side)
+        side.synchronize()
+        assert none is None and torch.equal(got, out)
+
+
+def test_chunk_attn_bad_device_data(ksa):
+    """Lengths outside the cache are clamped, offsets outside the tokens too, page ids outside the
+    pool are left out; each sets its flag and nothing faults."""
+    Hq, Hkv, D, bs = 4, 2, 64, 16
+    cache = Cache([100, 40], Hkv, D, bs, True, 4)
+    q = randn((30, Hq, D), 1)
+    cache.table[0, 2] = 10 ** 6
+    cache.table[0, 4] = -3
+    st = status()
+    out, _ = cache.call(ksa, q, i32([0, 20, 30]), i32([100, 40]), ksa.MASK_NONE, dev_status=st)
+    assert int(st) == 2
+    k, v = (torch.cat([x[:, :32], x[:, 48:64], x[:, 80:]], 1) for x in cache.rows[0])
+    want, _, mag = ref_attn(q[:20], k, v, 20, k.shape[1], False, D ** -0.5)
+    assert bool(((out[:20].double() - want).abs() <= (HALF + 4e-4) * mag + HALF * want.abs()).all())
+    cache = Cache([64, 64], Hkv, D, bs, False, 4, T=64)
+    full, _ = cache.call(ksa, q, i32([0, 20, 30]), i32([64, 64]), ksa.MASK_NONE)
+    for lens, cu in (([65, 2 ** 31 - 1], [0, 20, 30]), ([64, 64], [0, 20, 31]),
+                     ([64, 64], [-1, 20, 2 ** 31 - 1])):
+        st = status()
+        out, _ = cache.call(ksa, q, i32(cu), i32(lens), ksa.MASK_NONE, dev_status=st)
+        assert int(st) == 1 and torch.equal(out, full)
+    st = status()
+    out, _ = cache.call(ksa, q, i32([0, 20, 30]), i32([-5, 64]), ksa.MASK_NONE, dev_status=st)
+    assert int(st) == 1 and bool((out[:20] == 0).all()) and torch.equal(out[20:], full[20:])
+    st = status()
+    out = torch.full_like(q, 2.0)  # descending offsets: bounded, flagged, no token past N
+    cache.call(ksa, q, i32([0, 30, 10]), i32([64, 64]), ksa.MASK_NONE, out=out, dev_status=st)
+    assert int(st) == 1
+
+
+def test_chunk_attn_offsets_past_32_bits(ksa):
+    """Rows at the end of pools of more than 2^31 elements, paged and contiguous."""
+    Hkv, bs, D, L, n = 2, 64, 128, 200, 6
+    src = [randn((Hkv, 256, D), s) for s in (1, 2)]
+    q = randn((n, 4, D), 3)
+    want, _, mag = ref_attn(q, src[0][:, :L], src[1][:, :L], n, L, True, D ** -0.5)
+    P = 2 ** 31 // (Hkv * bs * D) + 9
+    K, V = (torch.empty((P, Hkv, bs, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ids = [P - 1, 0, P - 3, P - 2]
+    for x, s in zip((K, V), src):
+        for j, p in enumerate(ids):
+            x[p] = s[:, j * bs:(j + 1) * bs]
+    got, _ = ksa.ksa_chunk_attn_paged(q, K, V, i32([ids]), i32([0, n]), i32([L]))
+    assert bool(((got.double() - want).abs() <= (HALF + 4e-4) * mag + HALF * want.abs()).all())
+    del K, V
+    T = 2 ** 30 // (Hkv * D) + 256
+    K, V = (torch.empty((3, Hkv, T, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    for x, s in zip((K, V), src):
+        x[2, :, :256] = s
+    got, _ = ksa.ksa_chunk_attn(q, K, V, i32([0, 0, 0, n]), i32([0, 0, L]))
+    assert bool(((got.double() - want).abs() <= (HALF + 4e-4) * mag + HALF * want.abs()).all())
+
+
+def test_chunk_attn_single_tokens_agree_with_decode_attention(ksa):
+    """One query token per row: the dense decode attention's result."""
+    lens = [700, 16, 1, 2050]
+    cache = Cache(lens, 4, 128, 16, True, 6)
+    q = randn((4, 16, 128), 2)
+    lse = torch.empty((4, 16), device=DEV)
+    out, _ = cache.call(ksa, q, i32(range(5)), i32(lens), ksa.MASK_CAUSAL, lse=lse)
+    lse2 = torch.empty((4, 16), device=DEV)
+    want, _ = ksa.ksa_sparse_decode_attn_paged(q, cache.K, cache.V, cache.table, i32(lens),
+                                               lse=lse2)
+    for b, L in enumerate(lens):
+        _, _, mag = ref_attn(q[b:b + 1], *cache.rows[b], 1, L, True, 128 ** -0.5)
+        off = (out[b:b + 1].double() - want[b:b + 1].double()).abs()
+        assert bool((off <= 2 * (HALF + 4e-4) * mag + HALF * want[b:b + 1].abs()).all())
+    assert float((lse - lse2).abs().max()) <= 2e-4
+
+
+# ---------------------------------------------------------------------------
+# the operators as a serving loop uses them
+
+
+def test_serving_steps_end_to_end(ksa):
+    """Two prefill chunks and decode steps of a ragged batch: lengths -> pages and slots ->
+    rotary and cache write -> chunk attention, then summaries and the block-sparse decode step
+    (every block kept) on the same pages, every output against dense fp64 attention; then the
+    rows are released and their pages serve the next requests."""
+    Hq, Hkv, D, bs, B, mb = 8, 2, 128, 16, 3, 24
+    P = 40
+    rng = np.random.default_rng(1)
+    K, V = (torch.full((P, Hkv, bs, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+            for _ in range(2))
+    table = torch.full((B, mb), -1, dtype=torch.int32, device=DEV)
+    free = torch.from_numpy(rng.permutation(P).astype(np.int32)).to(DEV)
+    count, lens = i32([P]), torch.zeros(B, dtype=torch.int32, device=DEV)
+    freq = [1e6 ** (-i / 64) for i in range(64)]
+    axis = [i * 3 // 64 for i in range(64)]
+    rot, st = ksa.Rotary(freq, axis), status()
+    hist = [[], [], []]  # each row's (rotated k, v) so far, fp64 of the bf16 in the cache
+
+    def step(new, seed):
+        N = sum(new)
+        _, cu, slots, pos = ksa.ksa_assign_pages(lens, i32(new), table, free, count, bs, N + 2,
+                                                 seq_lens=lens, dev_status=st)
+        qkv = randn((N + 2, (Hq + 2 * Hkv) * D), seed)
+        q = qkv[:, :Hq * D].view(-1, Hq, D)
+        k = qkv[:, Hq * D:(Hq + Hkv) * D].view(-1, Hkv, D)
+        v = qkv[:, (Hq + Hkv) * D:].view(-1, Hkv, D)
+        p3 = torch.stack([pos, pos // 2, pos % 7])
+        qr = ksa.ksa_rotary_append_kv_paged(q, k, v, p3, slots, K, V, rot, dev_status=st)
+        c = cu.tolist()
+        assert c[-1] == N and slots[N:].tolist() == [-1, -1]
+        wk, mk = ref_rotary(k, p3, axis, freq, False)
+        for b in range(B):
+            for t in range(c[b], c[b + 1]):
+                s = int(slots[t])
+                row = K[s // bs, :, s % bs]
+                close_rotary(row[None], wk[t:t + 1], mk[t:t + 1], 64)
+                hist[b].append((row.clone(), v[t]))
+        return qr, cu, c
+
+    def check(out, qr, c, slack=0.0):
+        for b in range(B):
+            n = c[b + 1] - c[b]
+            if not n:
+                continue
+            k, v = (torch.stack([h[w] for h in hist[b]], 1) for w in (0, 1))
+            want, _, mag = ref_attn(qr[c[b]:c[b + 1]], k, v, n, len(hist[b]), True, D ** -0.5)
+            off = (out[c[b]:c[b + 1]].double() - want).abs()
+            assert bool((off <= (HALF + 4e-4) * mag + HALF * want.abs() + slack).all())
+
+    for new, seed in (([130, 1, 40], 1), ([5, 20, 0], 2)):
+        qr, cu, c = step(new, seed)
+        out, _ = ksa.ksa_chunk_attn_paged(qr, K, V, table, cu, lens, ksa.MASK_CAUSAL,
+                                          dev_status=st)
+        check(out, qr, c)
+    S = ksa.ksa_build_block_summaries_paged(K, table, lens, dev_status=st)
+    for seed in range(3, 6):
+        qr, cu, c = step([1, 1, 1], seed)
+        idx, cnt = ksa.ksa_decode_select_blocks_paged(qr[:B].contiguous(), K, table, S, lens, mb,
+                                                      dev_status=st)
+        out, _ = ksa.ksa_sparse_decode_attn_paged(qr[:B].contiguous(), K, V, table, lens, idx,
+                                                  cnt, tokens_per_idx=bs, dev_status=st)
+        check(out, qr, c)
+    assert int(st) == 0 and lens.tolist() == [138, 24, 43]
+    assert int(count) == P - (9 + 2 + 3)
+    ksa.ksa_release_pages(lens, i32([1, 0, 1]), table, free, count, bs, dev_status=st)
+    hist[0], hist[2] = [], []
+    qr, cu, c = step([33, 2, 1], 9)
+    out, _ = ksa.ksa_chunk_attn_paged(qr, K, V, table, cu, lens, ksa.MASK_CAUSAL, dev_status=st)
+    check(out, qr, c)
+    assert int(st) == 0 and int(count) == P - (3 + 2 + 1)
+
+
+def test_chunk_attn_captured_in_two_graphs(ksa):
+    """Two graphs on one workspace, replayed in turn: each gives the eager result."""
+    rows = [(3, 9000), (17, 400)]
+    cache, q, cu, out, lse = check_attn(ksa, rows, 8, 2, 128, 16, True, True, seed=31)
+    seq = i32([9000, 400])
+    ws = torch.zeros(ksa.ksa_chunk_attn_workspace(2, 8, 2, 128, cache.table.shape[1] * 16, 20),
+                     dtype=torch.uint8, device=DEV)
+    outs = [torch.zeros_like(out) for _ in range(2)]
+    masks = (ksa.MASK_CAUSAL, ksa.MASK_NONE)
+    eager = [cache.call(ksa, q, cu, seq, m, workspace=ws)[0] for m in masks]
+    torch.cuda.synchronize()
+    graphs = []
+    for m, o in zip(masks, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            cache.call(ksa, q, cu, seq, m, out=o, workspace=ws)
+    for _ in range(3):
+        for gr, o, want in zip(graphs, outs, eager):
+            o.fill_(-7.0)
+            gr.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want)
+    assert torch.equal(eager[0], out)
+    del graphs
