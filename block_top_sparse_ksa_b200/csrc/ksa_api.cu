@@ -163,6 +163,24 @@ bool encode_kv_tensor_map(CUtensorMap *map, const void *base, uint64_t rows, int
   return r == CUDA_SUCCESS;
 }
 
+bool encode_q_tensor_map(CUtensorMap *map, const void *base, int D, int Hq, int N,
+                         long long stride, int box_heads, int box_tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                              static_cast<cuuint64_t>(N)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2u,
+                                 static_cast<cuuint64_t>(stride) * 2u};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estride[3] = {1u, 1u, 1u};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+         estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace ksa
 
 extern "C" {

@@ -202,5 +202,9 @@ ksa_status set_last_error(ksa_status status, const char *fmt, ...)
 // TMA descriptor for a [rows, D] bf16 matrix, 128B swizzle, box = 64 x box_rows.
 bool encode_kv_tensor_map(CUtensorMap *map, const void *base, uint64_t rows, int D,
                           int box_rows);
+// TMA descriptor for queries [N, Hq, D] bf16 (token stride in elements), 128B
+// swizzle, box = 64 x box_heads x box_tokens.
+bool encode_q_tensor_map(CUtensorMap *map, const void *base, int D, int Hq, int N,
+                         long long stride, int box_heads, int box_tokens);
 
 }  // namespace ksa
