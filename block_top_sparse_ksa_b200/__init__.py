@@ -793,7 +793,9 @@ def _run_on(t: torch.Tensor, stream, fn, *args) -> None:
 
 def _scratch(ws: Optional[torch.Tensor], need: int, like: torch.Tensor) -> torch.Tensor:
     if ws is None:
-        return torch.zeros((max(int(need), 256),), dtype=torch.uint8, device=like.device)
+        ws = torch.empty((max(int(need), 256),), dtype=torch.uint8, device=like.device)
+        ws[:65536].zero_()  # the semaphores lie at the start; the rest needs no initial value
+        return ws
     if not ws.is_cuda or not ws.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
     return ws

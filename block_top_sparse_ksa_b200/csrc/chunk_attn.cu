@@ -11,16 +11,21 @@
 // (P then stays below 2^8 and l and O far inside fp32), so O is rescaled a few
 // times per row and not once per tile; the quotient O / l does not depend on m.
 //
-// Layout.  One CTA holds two streams, each with its S (whose first half P
-// overwrites) and O in tensor memory, four softmax warps of one row per thread:
-// no shuffles.  While one stream's softmax runs, the tensor cores work for the
-// other.  PAIR: the streams are two query tiles over the same key tiles.
-// Otherwise (few query rows per sequence) they are one query tile over the even
-// and the odd key tiles, joined at the end.  One warp loads (TMA; a page's rows
-// of one kv-head are one box), one issues the products.  Keys and values share
-// one ring of stages.  When there are fewer (tile, kv-head) pairs than SMs, the
-// keys are split between CTAs; the last CTA of a tile to finish joins the parts
-// in their order (so results do not depend on timing).
+// Layout.  One CTA per SM holds two streams, each with its S (whose first half
+// P overwrites) and O in tensor memory (2 x (128 + D) of 512 columns) and four
+// softmax warps of one row per thread: no shuffles.  While one stream's softmax
+// runs, the tensor cores work for the other.  PAIR: the streams are two query
+// tiles over the same key tiles.  Otherwise (few query rows per sequence) they
+// are one query tile over the even and the odd key tiles, joined at the end.
+// One warp loads (TMA; a page's rows of one kv-head are one box), one issues
+// the products, one hands out the work.  Keys and values share one ring.
+//
+// Work.  Items are (row, kv-head, tokens of a CTA), longest first within a row;
+// the CTAs stay and take the next item when they are done, so that an item's
+// loads and first product run under the epilogue of the one before.  Where the
+// items do not fill the SMs evenly, their keys are split into parts of `part`
+// tiles; the last CTA to finish a split item joins the parts in their order, so
+// results do not depend on timing.
 #include "ksa_device.cuh"
 #include "ksa_internal.h"
 #include "tcgen05_device.cuh"
@@ -29,45 +34,60 @@ namespace ksa {
 
 namespace {
 
-constexpr int kQ = 128;         // query rows of a tile
-constexpr int kKeys = 64;       // key tokens of a tile
-constexpr int kSoftWarps = 8;   // four per stream
-constexpr int kThreads = (kSoftWarps + 2) * 32;
-constexpr int kBadRing = 64;    // key tiles whose page marks are kept (above any stage count)
+constexpr int kQ = 128;        // query rows of a tile
+constexpr int kKeys = 128;     // key tokens of a tile
+constexpr int kSoftWarps = 8;  // four per stream
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kWorkWarp = 10;
+// A thread is launched with 65536 / 384 registers, 168.  The softmax keeps a row of 128 scores
+// in registers, so the third warpgroup passes its share on: 2 x 224 + 56 = 3 x 168.
+constexpr int kThreads = 384;
+constexpr int kSoftRegs = 224, kOtherRegs = 56;
+constexpr int kBadRing = 32;   // key tiles whose page marks are kept (above any stage count)
+constexpr int kWork = 2;       // items a CTA holds: the one it computes, and the next one
+constexpr int kPartsPerSm = 3;  // parts of split items, at most, per SM: the workspace's size
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLead = 4, kLag = 10;  // stagger of the weights' loop, in pairs of keys
-constexpr float kRescale = 8.f;  // log2 of the largest weight before m moves
+constexpr float kRescale = 8.f;      // log2 of the largest weight before m moves
+constexpr int kCtlBytes = 3072;
 
 template <int D, bool PAIR>
 struct Cfg {
   static constexpr int kQBytes = kQ * D * 2, kTileBytes = kKeys * D * 2;  // of a Q, of a K or V tile
   static constexpr int kQTiles = PAIR ? 2 : 1;
-  static constexpr int kFit = (224 * 1024 - kQTiles * kQBytes) / kTileBytes;
-  static constexpr int kStages = kFit < 20 ? kFit : 20;
-  static constexpr int kRows = kQ * kQTiles;  // query rows of a CTA
-  static constexpr int kAhead = PAIR ? 2 : 4;  // key tiles whose scores are in flight or in use
-  // 1 KB for the alignment of the tiles, the rest for barriers beside them
-  static constexpr int kSmem = kQTiles * kQBytes + kStages * kTileBytes + 1024 + 2048;
+  static constexpr int kStages = (224 * 1024 - kQTiles * kQBytes) / kTileBytes;
+  static constexpr int kRows = kQ * kQTiles;      // query rows of a CTA
+  static constexpr int kAhead = PAIR ? 1 : 2;     // key tiles whose scores are in use
+  static constexpr int kSmem = kQTiles * kQBytes + kStages * kTileBytes + kCtlBytes;
+};
+
+struct Work {
+  int b, g, token;   // row; kv-head; first token on the axis (-1: no more work)
+  int tokens;        // query tokens of the item
+  int seen;          // keys its first token sees (each further token one more when causal)
+  int len;           // L of the row
+  int t0, nt;        // key tiles of this part
+  int parts, slot, z;  // parts of the item, the first part's place in the workspace, this part
 };
 
 struct Ctl {  // in shared memory
-  uint64_t q_full, full[20], empty[20];
-  // per stream and score buffer: scores ready, weights ready, product with V done
-  uint64_t s_full[2][2], p_full[2][2], o_done[2][2], drain;
+  uint64_t q_full, q_empty, full[16], empty[16];
+  // per stream: scores ready, first half of the weights and all of them ready, product with V done
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+  uint64_t work_full[kWork], work_empty[kWork], soft, drain;
+  Work work[kWork];
   uint32_t tmem;
-  int abort, row, last;
+  int abort, last;
   uint32_t bad[kBadRing];
-};
-
-struct Plan {
-  int pair, tokens, slots, splits;  // tokens: query tokens of a CTA
+  float2 ml[2][kQ];  // m and l of the streams' rows, for their join
 };
 
 struct Params {
   ChunkArgs a;
-  uint32_t *sem;
-  float *part;
-  int tq, slots, splits;  // tq: query tokens of a tile
+  uint32_t *next, *done;  // items handed out beyond the first of each CTA; CTAs that have ended
+  uint32_t *sem;          // [max_parts] parts finished, at the item's first part
+  float *part;            // [max_parts] (m, l) of the rows, then O as [D / 4][rows][4]
+  int tq, max_parts;      // tq: query tokens of a tile
+  bool wide_out;          // out is 32-byte aligned
 };
 
 // Waits with a limit; false (and the CTA's abort mark) when it runs out.
@@ -95,11 +115,365 @@ __device__ __forceinline__ void exp2_in_place(uint32_t &x) {  // kept in program
   asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+r"(x));
 }
 
-// Offset of row b's first tile slot: rows b in order, each with at least
-// ceil(tokens / TT) slots, without a prefix sum over the rows.
-__device__ __forceinline__ int first_slot(const ChunkArgs &a, int b, int TT) {
-  return min(max(a.cu_q[b], 0), a.N) / TT + b;
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store_32(void *dst, const uint32_t *x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]),
+               "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
 }
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ---------------------------------------------------------------------------
+// the work warp: rows -> items -> parts
+
+struct Rows {  // 32 rows, one per lane
+  int b, s0, n, L;   // row; first token, tokens, cached tokens
+  int tiles, deep;   // CTAs' token groups; key tiles of the deepest one
+};
+
+__device__ __forceinline__ Rows load_rows(const ChunkArgs &a, int base, int TT, uint32_t *status) {
+  Rows r{};
+  const int b = base + static_cast<int>(threadIdx.x & 31);
+  if (b < a.B) {
+    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], L = a.seq_lens[b];
+    r.s0 = min(max(c0, 0), a.N);
+    r.n = max(0, min(c1, a.N) - r.s0);
+    r.L = min(max(L, 0), a.T);
+    if (c0 != r.s0 || c1 < c0 || c1 > a.N || (r.n > 0 && L != r.L))
+      flag_status(status, KSA_FLAG_SEQ_LEN_CLAMPED);
+    r.tiles = ceil_div(r.n, TT);
+    r.deep = r.n > 0 ? ceil_div(r.L, kKeys) : 0;
+  }
+  r.b = b;
+  return r;
+}
+
+// The lanes' rows in order of depth, deepest first, so that what is handed out last is short.
+__device__ __forceinline__ Rows sort_rows(const Rows &r) {
+  const int lane = threadIdx.x & 31;
+  const int after = __shfl_down_sync(0xffffffffu, r.deep, 1);
+  if (__all_sync(0xffffffffu, lane == 31 || r.deep >= after)) return r;
+  int rank = 0, src = 0;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    const int d = __shfl_sync(0xffffffffu, r.deep, i);
+    rank += d > r.deep || (d == r.deep && i < lane);
+  }
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i)
+    if (__shfl_sync(0xffffffffu, rank, i) == lane) src = i;
+  return {__shfl_sync(0xffffffffu, r.b, src),     __shfl_sync(0xffffffffu, r.s0, src),
+          __shfl_sync(0xffffffffu, r.n, src),     __shfl_sync(0xffffffffu, r.L, src),
+          __shfl_sync(0xffffffffu, r.tiles, src), __shfl_sync(0xffffffffu, r.deep, src)};
+}
+
+// What is cut: items before `whole` are not, the others into parts of `part` key tiles.
+struct Cut {
+  int whole, part;
+};
+
+// Lane i < 16 tries all items with the deepest cut into i + 1 parts (lane 15: as many as fill the
+// SMs), lane i >= 16 whole items but for the last round that does not fill the SMs, cut into
+// i - 14 parts; every CTA gets the same answer.  Estimated ends, in key tiles (some 1.8 us): a part
+// costs kStart more for its start and end, kPart again if it is joined, and the last join
+// `join` (measured: 28 us for the 256 rows of a pair and 4 parts, 10 us for a few rows).  Equal
+// items go round by round, unequal ones fill the SMs evenly but for a third of a part.
+__device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first, int TT, int ctas,
+                                          int max_parts, float join) {
+  constexpr float kStart = 2.5f, kPart = 1.5f;
+  const int lane = threadIdx.x & 31;
+  float tiles = 0.f, items = 0.f;
+  int deepest = 0;
+  Rows r = first;
+  for (int base = 0; base < a.B; base += 32) {
+    if (base > 0) r = load_rows(a, base, TT, nullptr);
+    const float k = static_cast<float>(r.tiles) * a.Hkv;
+    // mean depth of the row's groups: from the first group's last token to the last one's
+    const int top = a.causal ? ceil_div(max(0, r.L - r.n + min(r.n, TT)), kKeys) : r.deep;
+    items += k;
+    tiles += k * 0.5f * (top + r.deep);
+    deepest = max(deepest, r.deep);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
+    items += __shfl_xor_sync(0xffffffffu, items, off);
+  }
+  deepest = __reduce_max_sync(0xffffffffu, deepest);
+  if (deepest < 4 || items == 0.f || items > 1e6f) return {0, max(deepest, 1)};
+  const int n = static_cast<int>(items), rem = n % ctas;
+  const float mean = tiles / items;
+  const bool equal = mean >= 0.85f * deepest;
+  const int cuts = lane < 15 ? lane + 1 : lane == 15 ? max(1, ctas / n) : lane - 14;
+  const int s = max(2, ceil_div(deepest, cuts));
+  float parts = 0.f, joined = 0.f;  // of cutting all items
+  if (a.B <= 32) {
+    const float own = static_cast<float>(first.tiles) * a.Hkv, per = 1.f / s;
+    const int deep = first.deep;
+#pragma unroll 4
+    for (int b = 0; b < a.B; ++b) {
+      const float k = __shfl_sync(0xffffffffu, own, b);
+      const float c = ceilf(__shfl_sync(0xffffffffu, deep, b) * per);
+      parts += k * fmaxf(c, 1.f);
+      if (c > 1.f) joined += k * c;
+    }
+  } else {  // all rows as deep as the mean
+    const float c = fmaxf(1.f, ceilf(mean / s));
+    parts = items * c;
+    joined = s < deepest ? parts : 0.f;
+  }
+  float cost;
+  if (lane < 16) {
+    cost = equal ? ceilf(parts / ctas) * (tiles / parts + kStart + (joined > 0.f ? kPart : 0.f))
+                 : fmaxf((tiles + kStart * parts + kPart * joined) / ctas + 0.35f * min(s, deepest),
+                         s + kStart);
+    if (joined > 0.f) cost += join;
+  } else {
+    joined = static_cast<float>(rem) * cuts;
+    cost = equal && rem > 0 && n > ctas
+               ? (n / ctas) * (mean + kStart) +
+                     ceilf(joined / ctas) * (mean / cuts + kStart + kPart) + join
+               : INFINITY;
+  }
+  if (joined > max_parts) cost = INFINITY;
+  if (lane == 0) cost *= 0.95f;
+  float best = cost;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    best = fminf(best, __shfl_xor_sync(0xffffffffu, best, off));
+  const int who = __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1;
+  return {who < 16 ? 0 : n - rem, __shfl_sync(0xffffffffu, s, who)};
+}
+
+// Inclusive prefix sum over the warp.
+__device__ __forceinline__ int warp_scan(int x) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if (static_cast<int>(threadIdx.x & 31) >= off) x += y;
+  }
+  return x;
+}
+
+__device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT, Rows r) {
+  const ChunkArgs &a = p.a;
+  const int lane = threadIdx.x & 31;
+  const int ctas = static_cast<int>(gridDim.x);
+  uint32_t *status = blockIdx.x == 0 ? a.status : nullptr;
+  for (int base = 32; status != nullptr && base < a.B; base += 32) load_rows(a, base, TT, status);
+  Cut cut = choose_cut(a, r, TT, ctas, p.max_parts, TT > p.tq ? 12.f : 5.f);
+  {  // the choice was an estimate: the workspace must hold the real parts
+    float joined = 0.f;
+    Rows q = r;
+    for (int b = 0; b < a.B; b += 32) {
+      if (b > 0) q = load_rows(a, b, TT, nullptr);
+      const int c = ceil_div(q.deep, cut.part);
+      joined += c > 1 ? static_cast<float>(q.tiles) * a.Hkv * c : 0.f;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) joined += __shfl_xor_sync(0xffffffffu, joined, off);
+    // (of whole items before a cut tail only the tail counts: at most `rem` items, see above)
+    if (cut.whole == 0 && joined > p.max_parts) cut = {0, a.T};
+  }
+  // the current 32 rows: parts [first, first + sum of units), whole items, places of parts to join
+  int base = 0, first = 0, first_item = 0, first_slot = 0;
+  int cuts, whole, units, slots, units_end, slots_end;
+  auto measure = [&]() {
+    r = sort_rows(r);
+    const int items = r.tiles * a.Hkv, end = warp_scan(items);
+    cuts = max(1, ceil_div(r.deep, cut.part));
+    whole = cuts == 1 ? items : min(max(cut.whole - (first_item + end - items), 0), items);
+    units = whole + (items - whole) * cuts;
+    slots = units - whole;
+    units_end = warp_scan(units);
+    slots_end = warp_scan(slots);
+    first_item += __shfl_sync(0xffffffffu, end, 31);
+  };
+  measure();
+  int id = static_cast<int>(blockIdx.x), at = 0;
+  uint32_t turn = 1;
+  while (true) {
+    int sum = __shfl_sync(0xffffffffu, units_end, 31);
+    while (id >= first + sum && base + 32 < a.B) {
+      first += sum;
+      first_slot += __shfl_sync(0xffffffffu, slots_end, 31);
+      base += 32;
+      r = load_rows(a, base, TT, nullptr);
+      measure();
+      sum = __shfl_sync(0xffffffffu, units_end, 31);
+    }
+    const bool end = id >= first + sum;
+    int next = 0;
+    if (!end && lane == 0) next = ctas + static_cast<int>(atomicAdd(p.next, 1u));
+    Work w{};
+    w.token = -1;
+    bool use = true;
+    if (!end) {
+      const int local = id - first;
+      const int who = __ffs(__ballot_sync(0xffffffffu, local < units_end)) - 1;
+      const int c = __shfl_sync(0xffffffffu, cuts, who),
+                tiles = __shfl_sync(0xffffffffu, r.tiles, who),
+                n = __shfl_sync(0xffffffffu, r.n, who), L = __shfl_sync(0xffffffffu, r.L, who);
+      const int in_row = local - __shfl_sync(0xffffffffu, units_end - units, who);
+      const int slot0 = first_slot + __shfl_sync(0xffffffffu, slots_end - slots, who);
+      const int uncut = __shfl_sync(0xffffffffu, whole, who);
+      const bool is_cut = in_row >= uncut;
+      const int item = is_cut ? uncut + (in_row - uncut) / c : in_row;
+      const int tile = tiles - 1 - item / a.Hkv;  // when causal, the deepest first
+      w.z = is_cut ? (in_row - uncut) % c : 0;
+      w.g = item % a.Hkv;
+      w.b = __shfl_sync(0xffffffffu, r.b, who);
+      w.token = __shfl_sync(0xffffffffu, r.s0, who) + tile * TT;
+      w.tokens = min(TT, n - tile * TT);
+      w.seen = a.causal ? L - n + tile * TT + 1 : L;
+      w.len = L;
+      const int kend = a.causal ? max(0, w.seen + w.tokens - 1) : L;
+      const int all = ceil_div(kend, kKeys), s = is_cut ? cut.part : max(all, 1);
+      w.t0 = w.z * s;
+      w.nt = min(s, all - w.t0);
+      w.parts = max(1, ceil_div(all, s));
+      w.slot = is_cut ? slot0 + (item - uncut) * c : 0;
+      use = w.z < w.parts;
+    }
+    if (use) {
+      if (!wait_bar(&ctl.work_empty[at], turn, &ctl.abort)) return;
+      if (lane == 0) {
+        ctl.work[at] = w;
+        mbar_arrive(&ctl.work_full[at]);
+      }
+      __syncwarp();
+      if (++at == kWork) {
+        at = 0;
+        turn ^= 1u;
+      }
+    }
+    if (end) return;
+    id = __shfl_sync(0xffffffffu, next, 0);
+  }
+}
+
+// The next item, for a warp: waits until it is there; false after an aborted wait.
+struct Take {
+  int at = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ bool get(Ctl &ctl, Work &w) {
+    const bool ok = wait_bar(&ctl.work_full[at], turn, &ctl.abort);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    w = ctl.work[at];
+    return true;
+  }
+  __device__ __forceinline__ void release(Ctl &ctl) {  // the warp reads the item no more
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.work_empty[at]);
+    if (++at == kWork) {
+      at = 0;
+      turn ^= 1u;
+    }
+  }
+};
+
+// The join of an item's parts, by the softmax warps.  First each row's (m, 1 / l) over the parts,
+// in their order, and its lse.
+template <int D, bool PAIR>
+__device__ __noinline__ void join_stats(const Params &p, const Work &w, float2 *stats, int TQ,
+                                        int G, float c) {
+  const ChunkArgs &a = p.a;
+  constexpr int kRows = Cfg<D, PAIR>::kRows;
+  constexpr size_t pitch = kRows * (D + 2);
+  const float *base = p.part + static_cast<size_t>(w.slot) * pitch;
+  const int rows = w.tokens * G, parts = w.parts;
+  for (int rr = threadIdx.x; rr < rows; rr += kSoftWarps * 32) {
+    const int tok = rr / G, hh = rr % G;
+    const int row = (PAIR ? (tok / TQ) * kQ + (tok % TQ) * G : tok * G) + hh;
+    float m = -INFINITY, l = 0.f;
+    for (int q0 = 0; q0 < parts; q0 += 16) {  // 16 parts in flight
+      float2 ml[16];
+      float up = m;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        ml[q] = make_float2(-INFINITY, 0.f);
+        if (q0 + q < parts)
+          ml[q] = __ldcg(reinterpret_cast<const float2 *>(base + (q0 + q) * pitch) + row);
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) up = fmaxf(up, ml[q].x);
+      if (m != -INFINITY) l *= fast_exp2((m - up) * c);
+      m = up;
+      // a part that saw nothing has m = -inf, l = 0; one with a NaN score l = NaN
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        l += ml[q].x == -INFINITY ? ml[q].y : ml[q].y * fast_exp2((ml[q].x - m) * c);
+    }
+    stats[rr] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
+    if (a.lse != nullptr)
+      a.lse[(static_cast<long long>(w.token) + tok) * a.Hq + w.g * G + hh] =
+          l == 0.f ? -INFINITY : m * a.scale + logf(l);
+  }
+}
+
+// ... and the outputs, after the warps have met.  A thread adds up 4 dims of a row at a time, parts
+// in order, 4 parts of 4 such quads in flight: the parts come out of L2, some 700 cycles away.
+template <int D, bool PAIR>
+__device__ __noinline__ void join_outputs(const Params &p, const Work &w, const float2 *stats,
+                                          int TQ, int G, float c) {
+  const ChunkArgs &a = p.a;
+  constexpr int kRows = Cfg<D, PAIR>::kRows, kThr = kSoftWarps * 32, kQuads = 4;
+  constexpr size_t pitch = kRows * (D + 2);
+  const float *base = p.part + static_cast<size_t>(w.slot) * pitch;
+  const int rows = w.tokens * G, work = rows * (D / 4), parts = w.parts;
+  for (int e0 = threadIdx.x; e0 < work; e0 += kThr * kQuads) {
+    const float *src[kQuads];  // m of the row in the first part, and where its quad begins
+    int quad[kQuads];
+    float2 st[kQuads];
+    float4 o[kQuads];
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      const int e = min(e0 + i * kThr, work - 1), rr = e % rows, tok = rr / G, hh = rr % G;
+      const int row = (PAIR ? (tok / TQ) * kQ + (tok % TQ) * G : tok * G) + hh;
+      src[i] = base + 2 * row;
+      quad[i] = 2 * kRows + (e / rows) * 4 * kRows + 4 * row - 2 * row;
+      st[i] = stats[rr];
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int q0 = 0; q0 < parts; q0 += 4) {
+      float m[4][kQuads];
+      float4 x[4][kQuads];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const size_t off = static_cast<size_t>(min(q0 + q, parts - 1)) * pitch;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          m[q][i] = __ldcg(src[i] + off);
+          x[q][i] = __ldcg(reinterpret_cast<const float4 *>(src[i] + off + quad[i]));
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          const bool none = q0 + q >= parts || m[q][i] == -INFINITY;
+          const float f = none ? 0.f : fast_exp2((m[q][i] - st[i].x) * c) * st[i].y;
+          o[i].x += x[q][i].x * f;
+          o[i].y += x[q][i].y * f;
+          o[i].z += x[q][i].z * f;
+          o[i].w += x[q][i].w * f;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      const int e = e0 + i * kThr;
+      if (e >= work) break;
+      const int rr = e % rows, tok = rr / G, hh = rr % G;
+      const long long at = (static_cast<long long>(w.token) + tok) * a.Hq + w.g * G + hh;
+      *reinterpret_cast<uint2 *>(a.out + at * D + (e / rows) * 4) =
+          make_uint2(pack_bf16x2(o[i].x, o[i].y), pack_bf16x2(o[i].z, o[i].w));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 
 template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -108,122 +482,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ Params p) {
   using C = Cfg<D, PAIR>;
-  constexpr int NST = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *tiles = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  Ctl &ctl = *reinterpret_cast<Ctl *>(tiles + C::kQTiles * C::kQBytes + NST * C::kTileBytes);
-  static_assert(sizeof(Ctl) <= 2048 && NST <= 20 && NST < kBadRing, "");
+  constexpr int NST = C::kStages, A = C::kAhead;
+  extern __shared__ __align__(1024) uint8_t tiles[];
+  uint8_t *ring = tiles + C::kQTiles * C::kQBytes;
+  Ctl &ctl = *reinterpret_cast<Ctl *>(ring + NST * C::kTileBytes);
+  static_assert(sizeof(Ctl) <= kCtlBytes && NST <= 16, "");
+  static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168 && C::kSmem <= 227 * 1024, "");
   const ChunkArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv, TQ = p.tq, TT = TQ * C::kQTiles;
 
-  // slots run backwards: a row's last tiles see the most keys when causal
-  int x = blockIdx.x;
-  const int z = x / (p.slots * a.Hkv);
-  x -= z * p.slots * a.Hkv;
-  const int g = x / p.slots, slot = p.slots - 1 - (x - g * p.slots);
-
-  if (blockIdx.x == 0) {
-    for (int b = tid; b < a.B; b += kThreads)
-      if (a.cu_q[b] < 0 || a.cu_q[b] > a.cu_q[b + 1] || a.cu_q[b + 1] > a.N)
-        flag_status(a.status, KSA_FLAG_SEQ_LEN_CLAMPED);
-  }
-  if (warp == 0) {  // the row of this slot: 32-way search
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-      const bool le = at < hi && first_slot(a, at, TT) <= slot;
-      const uint32_t no = ~__ballot_sync(0xffffffffu, le);
-      const int cnt = no == 0u ? 32 : __ffs(no) - 1;
-      lo += cnt * step;
-      hi = min(hi, lo + step);
-    }
-    if (lane == 0) {
-      ctl.row = lo;
-      ctl.abort = 0;
-    }
-  } else if (warp == kSoftWarps) {
+  if (warp == kMmaWarp) {
     if (lane == 0) {
       mbar_init(&ctl.q_full, 1);
+      mbar_init(&ctl.q_empty, 1);
       for (int i = 0; i < NST; ++i) {
         mbar_init(&ctl.full[i], 1);
         mbar_init(&ctl.empty[i], 1);
       }
       for (int s = 0; s < 2; ++s) {
-        for (int i = 0; i < 2; ++i) {
-          mbar_init(&ctl.s_full[s][i], 1);
-          mbar_init(&ctl.p_full[s][i], 4);
-          mbar_init(&ctl.o_done[s][i], 1);
-        }
+        mbar_init(&ctl.s_full[s], 1);
+        mbar_init(&ctl.p_half[s], 4);
+        mbar_init(&ctl.p_full[s], 4);
+        mbar_init(&ctl.o_done[s], 1);
       }
+      for (int i = 0; i < kWork; ++i) {
+        mbar_init(&ctl.work_full[i], 1);
+        mbar_init(&ctl.work_empty[i], kSoftWarps + 2);
+      }
+      mbar_init(&ctl.soft, kSoftWarps);
       mbar_init(&ctl.drain, 1);
+      ctl.abort = 0;
       fence_mbar_init();
     }
-  } else if (warp == kSoftWarps + 1) {
-    if (lane == 0) {
-      prefetch_tensormap(&q_map);
-      prefetch_tensormap(&k_map);
-      prefetch_tensormap(&v_map);
-    }
+    __syncwarp();
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_fence_before();
+  } else if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
   }
+  Rows rows{};
+  if (warp == kWorkWarp)  // one CTA reports the rows' flags
+    rows = load_rows(a, 0, TT, blockIdx.x == 0 ? a.status : nullptr);
   __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = ctl.tmem;
 
-  const int b = ctl.row;
-  const int s0 = min(max(a.cu_q[b], 0), a.N), s1 = max(s0, min(a.cu_q[b + 1], a.N));
-  const int n = s1 - s0, tok0 = (slot - (s0 / TT + b)) * TT;  // first token, within the row
-  if (tok0 < 0 || tok0 >= n) return;
-  const int L0 = a.seq_lens[b], L = min(max(L0, 0), a.T);
-  if (L != L0 && tid == 0) flag_status(a.status, KSA_FLAG_SEQ_LEN_CLAMPED);
-  const int tokens = min(TT, n - tok0);  // of this CTA
-  // keys that the CTA's last token sees, in tiles, and this CTA's share of them
-  const int kend = a.causal ? max(0, L - n + tok0 + tokens) : L;
-  const int all = (kend + kKeys - 1) / kKeys, share = (all + p.splits - 1) / p.splits;
-  const int parts = share == 0 ? 1 : (all + share - 1) / share;
-  if (z >= parts) return;
-  const int t0 = z * share, nt = min(share, all - t0);
-  const int q_tiles = PAIR && tokens > TQ ? 2 : 1;
-
-  uint32_t tmem = 0;
-  if (nt > 0) {
-    if (warp == kSoftWarps) {
-      tmem_alloc(&ctl.tmem, 512);
-      tmem_fence_before();
-    }
-    __syncthreads();
-    tmem_fence_after();
-    tmem = ctl.tmem;
-  }
-  uint8_t *ring = tiles + C::kQTiles * C::kQBytes;
-
-  // the ring's order is the order of use: K0 ... K(A-1), V0, K(A), V1, K(A+1), ...
-  constexpr int A = C::kAhead;
-
-  if (nt > 0 && warp == kSoftWarps + 1) {
+  if (warp == kWorkWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    hand_out_work(p, ctl, TT, rows);
+  } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&ctl.q_full, static_cast<uint32_t>(q_tiles * G * TQ * D * 2));
-      for (int s = 0; s < q_tiles; ++s)
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_3d(tiles + s * C::kQBytes + h * (kQ * 128), &q_map, h * 64, g * G,
-                      s0 + tok0 + s * TQ, &ctl.q_full);
-    }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const bool paged = a.kv.table != nullptr;
     const int bs = paged ? a.kv.bs : kKeys, ppt = kKeys / bs;  // boxes of a tile and half
     const int groups = 32 / ppt;                               // tiles whose ids 32 lanes hold
     const int box = lane % ppt, half = lane / ppt;
-    const long long rows =
+    const int none = static_cast<int>(  // a row past the pool: the box reads as zeros
         paged ? static_cast<long long>(a.kv.num_pages) * a.Hkv * bs
-              : static_cast<long long>(a.B) * a.Hkv * a.T;
-    const int none = static_cast<int>(rows);  // a row past the pool: the box reads as zeros
-    const int32_t *table = paged ? a.kv.table + static_cast<size_t>(b) * a.kv.max_blocks : nullptr;
-    const int blocks = (kend + bs - 1) / bs;
-    auto load_ids = [&](int group) {  // the page of block (t0 + group * groups) * ppt + lane
-      const int j = (t0 + group * groups) * ppt + lane;
-      return paged && j < blocks && j < a.kv.max_blocks ? __ldg(table + j) : -1;
-    };
-    int ids = load_ids(0), next = load_ids(1);
-    int stage = 0, puts = 0;
-    uint32_t drained = 1;  // a place's first filling waits for nothing
+              : static_cast<long long>(a.B) * a.Hkv * a.T);
+    int stage = 0, puts = 0, mark = 0;
+    uint32_t drained = 1, q_turn = 1;  // a place's first filling waits for nothing
     bool ok = true;
     auto put = [&](const CUtensorMap *map, int y) {  // one tile into the next place
       ok = wait_bar(&ctl.empty[stage], drained, &ctl.abort);
@@ -240,52 +561,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         drained ^= 1u;
       }
     };
-    // K runs A tiles ahead of V; the rows of the tiles between wait in registers
-    int group = 0, y_ring[A];
-    for (int j = 0; j < nt + A && ok; ++j) {
-      if (j >= A) put(&v_map, y_ring[0]);  // of tile j - A
-#pragma unroll
-      for (int i = 0; i + 1 < A; ++i) y_ring[i] = y_ring[i + 1];
-      if (j >= nt || !ok) continue;
-      int y = none;
-      if (paged) {
-        if (j / groups != group) {
-          ids = next;
-          next = load_ids(++group + 1);
+    Take take;
+    Work w;
+    while (ok && take.get(ctl, w) && w.token >= 0) {
+      const int32_t *table =
+          paged ? a.kv.table + static_cast<size_t>(w.b) * a.kv.max_blocks : nullptr;
+      const int kend = a.causal ? max(0, w.seen + w.tokens - 1) : w.len;
+      const int blocks = ceil_div(kend, bs);
+      auto load_ids = [&](int group) {  // the page of block (t0 + group * groups) * ppt + lane
+        const int j = (w.t0 + group * groups) * ppt + lane;
+        return paged && j < blocks && j < a.kv.max_blocks ? __ldg(table + j) : -1;
+      };
+      int ids = load_ids(0), next = load_ids(1), group = 0;
+      int y_ring[A];  // K runs A tiles ahead of V; the rows of the tiles between
+      for (int j = 0; j < w.nt + A && ok; ++j) {
+        if (j == A) {  // the first keys are on their way: now the queries
+          ok = wait_bar(&ctl.q_empty, q_turn, &ctl.abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          q_turn ^= 1u;
+          const int q_tiles = PAIR && w.tokens > TQ ? 2 : 1;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&ctl.q_full, static_cast<uint32_t>(q_tiles * G * TQ * D * 2));
+            for (int s = 0; s < q_tiles; ++s)
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(tiles + s * C::kQBytes + h * (kQ * 128), &q_map, h * 64, w.g * G,
+                            w.token + s * TQ, &ctl.q_full);
+          }
+          __syncwarp();
         }
-        const int block = (t0 + j) * ppt + box;
-        const int id = __shfl_sync(0xffffffffu, ids, (j % groups) * ppt + box);
-        const bool inside = block < blocks, good = id >= 0 && id < a.kv.num_pages;
-        if (inside && good) y = (id * a.Hkv + g) * bs;
-        const uint32_t bad = __ballot_sync(0xffffffffu, lane < ppt && inside && !good);
+        if (j >= A) put(&v_map, y_ring[0]);  // of tile j - A
+#pragma unroll
+        for (int i = 0; i + 1 < A; ++i) y_ring[i] = y_ring[i + 1];
+        if (j >= w.nt || !ok) continue;
+        int y = none;
+        uint32_t bad = 0u;
+        if (paged) {
+          if (j / groups != group) {
+            ids = next;
+            next = load_ids(++group + 1);
+          }
+          const int block = (w.t0 + j) * ppt + box;
+          const int id = __shfl_sync(0xffffffffu, ids, (j % groups) * ppt + box);
+          const bool inside = block < blocks, good = id >= 0 && id < a.kv.num_pages;
+          if (inside && good) y = (id * a.Hkv + w.g) * bs;
+          bad = __ballot_sync(0xffffffffu, lane < ppt && inside && !good);
+        } else {
+          y = (w.b * a.Hkv + w.g) * a.T + (w.t0 + j) * kKeys;
+        }
         if (lane == 0) {
-          ctl.bad[j % kBadRing] = bad;
+          ctl.bad[mark] = bad;
           if (bad != 0u) flag_status(a.status, KSA_FLAG_INDEX_SKIPPED);
         }
-      } else {
-        y = (b * a.Hkv + g) * a.T + (t0 + j) * kKeys;
-        if (lane == 0) ctl.bad[j % kBadRing] = 0u;
+        mark = (mark + 1) % kBadRing;
+        put(&k_map, y);
+        y_ring[A - 1] = y;
       }
-      put(&k_map, y);
-      y_ring[A - 1] = y;
+      take.release(ctl);
     }
     // leave no copy in flight behind (also after an aborted wait)
-    for (int i = max(0, puts - NST); i < puts; ++i)
-      wait_bar(&ctl.full[i % NST], (i / NST) & 1, &ctl.abort);
-    wait_bar(&ctl.q_full, 0, &ctl.abort);
-  } else if (nt > 0 && warp == kSoftWarps) {
+    for (int i = max(0, puts - NST); i < puts; ++i) mbar_wait(&ctl.full[i % NST], (i / NST) & 1);
+    mbar_wait(&ctl.q_full, q_turn);
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     constexpr uint32_t idesc_s = mma_idesc_bf16(kQ, kKeys, false);
     constexpr uint32_t idesc_o = mma_idesc_bf16(kQ, D, true);
-    bool ok = wait_bar(&ctl.q_full, 0, &ctl.abort);
-    const int streams = PAIR ? q_tiles : 2;
     const uint64_t q_desc = smem_desc_128b(smem_addr(tiles), 16, 1024);
     const uint64_t k_desc = smem_desc_128b(smem_addr(ring), 16, 1024);
     const uint64_t v_desc = smem_desc_128b(smem_addr(ring), kKeys * 128, 1024);
     const uint32_t one = elect_one();
-    int stage = 0;  // next place of the ring, and the parity of its filling
-    uint32_t fill = 0;
-    auto take = [&]() {  // waits for the next place and returns it
+    int stage = 0;                     // next place of the ring, and the parity of its filling
+    uint32_t fill = 0, q_turn = 0;
+    uint32_t p_turn[2] = {0, 0};       // parity of each stream's next weights
+    bool ok = true;
+    auto next_place = [&]() {  // waits for it
       const int st = stage;
       ok = ok && wait_bar(&ctl.full[st], fill, &ctl.abort);
       if (++stage == NST) {
@@ -294,365 +644,384 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return st;
     };
-    // scores of stream s's k-th tile, its keys in place st: to buffer k % 2
-    auto scores = [&](int s, int k, int st) {
-      const uint64_t qd = q_desc + static_cast<uint64_t>((PAIR ? s : 0) * C::kQBytes >> 4);
-      const uint64_t kd = k_desc + static_cast<uint64_t>(st * C::kTileBytes >> 4);
-      const uint32_t to = tmem + s * 2 * kKeys + (k & 1) * kKeys;
+    Take take;
+    Work w;
+    while (ok && take.get(ctl, w) && w.token >= 0) {
+      take.release(ctl);
+      if (w.nt == 0) continue;
+      const int streams = PAIR ? (w.tokens > TQ ? 2 : 1) : 2;
+      // scores of stream s's next tile, its keys in place st
+      auto scores = [&](int s, int st) {
+        const uint64_t qd = q_desc + static_cast<uint64_t>((PAIR ? s : 0) * C::kQBytes >> 4);
+        const uint64_t kd = k_desc + static_cast<uint64_t>(st * C::kTileBytes >> 4);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        mma_ss(one, to, qd + static_cast<uint64_t>(((i / 4) * (kQ * 128) + (i % 4) * 32) >> 4),
-               kd + static_cast<uint64_t>(((i / 4) * (kKeys * 128) + (i % 4) * 32) >> 4), idesc_s,
-               i > 0);
-      mma_commit(one, &ctl.s_full[s][k & 1]);
-      if (!PAIR || s == streams - 1) mma_commit(one, &ctl.empty[st]);
-    };
-    for (int j = 0; j < min(A, nt); ++j) {
-      const int st = take();
-      if (!ok) break;
-      tmem_fence_after();
-      if (PAIR)
-        for (int s = 0; s < streams; ++s) scores(s, j, st);
-      else
-        scores(j & 1, j >> 1, st);
-    }
-    for (int j = 0; j < nt && ok; ++j) {
-      const int sv = take();
-      int sk = 0;
-      if (!ok) break;
-      if ((t0 + j + 1) * kKeys > L) {
-        // the cache behind the row's last token: P is 0 there, but 0 x NaN is not
-        const int r0 = L - (t0 + j) * kKeys;
-        for (int e = r0 * 8 + lane; e < kKeys * 8; e += 32)
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            *reinterpret_cast<uint4 *>(ring + sv * C::kTileBytes + h * (kKeys * 128) + e * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      const uint64_t vd = v_desc + static_cast<uint64_t>(sv * C::kTileBytes >> 4);
-      const int k = PAIR ? j : j >> 1;
-      for (int i = 0; i < (PAIR ? streams : 1); ++i) {
-        const int s = PAIR ? i : j & 1;
-        ok = wait_bar(&ctl.p_full[s][k & 1], (k >> 1) & 1, &ctl.abort);
+        for (int i = 0; i < D / 16; ++i)
+          mma_ss(one, tmem + s * kKeys,
+                 qd + static_cast<uint64_t>(((i / 4) * (kQ * 128) + (i % 4) * 32) >> 4),
+                 kd + static_cast<uint64_t>(((i / 4) * (kKeys * 128) + (i % 4) * 32) >> 4), idesc_s,
+                 i > 0);
+        mma_commit(one, &ctl.s_full[s]);
+        if (!PAIR || s == streams - 1) mma_commit(one, &ctl.empty[st]);
+      };
+      for (int j = 0; j < min(A, w.nt); ++j) {
+        const int st = next_place();
+        if (j == 0) {
+          ok = ok && wait_bar(&ctl.q_full, q_turn, &ctl.abort);
+          q_turn ^= 1u;
+        }
         if (!ok) break;
         tmem_fence_after();
+        if (PAIR)
+          for (int s = 0; s < streams; ++s) scores(s, st);
+        else
+          scores(j, st);
+      }
+      if (w.nt <= A) mma_commit(one, &ctl.q_empty);
+      for (int j = 0; j < w.nt && ok; ++j) {
+        const int sv = next_place();
+        int sk = 0;
+        if (!ok) break;
+        if ((w.t0 + j + 1) * kKeys > w.len) {
+          // the cache behind the row's last token: P is 0 there, but 0 x NaN is not
+          const int r0 = w.len - (w.t0 + j) * kKeys;
+          for (int e = r0 * 8 + lane; e < kKeys * 8; e += 32)
 #pragma unroll
-        for (int e = 0; e < kKeys / 16; ++e)
-          mma_ts(one, tmem + 4 * kKeys + s * D, tmem + s * 2 * kKeys + (k & 1) * kKeys + e * 8,
-                 vd + static_cast<uint64_t>(e * 16 * 128 >> 4), idesc_o, k > 0 || e > 0);
-        mma_commit(one, &ctl.o_done[s][k & 1]);
-        if (!PAIR || s == streams - 1) mma_commit(one, &ctl.empty[sv]);
-        if (j + A < nt) {
-          if (i == 0) sk = take();
+            for (int h = 0; h < D / 64; ++h)
+              *reinterpret_cast<uint4 *>(ring + sv * C::kTileBytes + h * (kKeys * 128) + e * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint64_t vd = v_desc + static_cast<uint64_t>(sv * C::kTileBytes >> 4);
+        const bool first = PAIR ? j == 0 : j < 2;  // of its stream
+        for (int i = 0; i < (PAIR ? streams : 1); ++i) {
+          const int s = PAIR ? i : j & 1;
+          for (int half = 0; half < 2 && ok; ++half) {
+            ok = wait_bar(half == 0 ? &ctl.p_half[s] : &ctl.p_full[s],
+                          s == 0 ? p_turn[0] : p_turn[1], &ctl.abort);
+            if (!ok) break;
+            tmem_fence_after();
+#pragma unroll
+            for (int e = 0; e < kKeys / 32; ++e) {
+              const int x = half * (kKeys / 32) + e;
+              mma_ts(one, tmem + 2 * kKeys + s * D, tmem + s * kKeys + x * 8,
+                     vd + static_cast<uint64_t>(x * 16 * 128 >> 4), idesc_o, !first || x > 0);
+            }
+          }
           if (!ok) break;
-          tmem_fence_after();
-          scores(s, k + 2, sk);
+          if (s == 0)
+            p_turn[0] ^= 1u;
+          else
+            p_turn[1] ^= 1u;
+          mma_commit(one, &ctl.o_done[s]);
+          if (!PAIR || s == streams - 1) mma_commit(one, &ctl.empty[sv]);
+          if (j + A < w.nt) {
+            if (i == 0) sk = next_place();
+            if (!ok) break;
+            tmem_fence_after();
+            scores(s, sk);
+            if (j + A + 1 == w.nt && (!PAIR || s == streams - 1)) mma_commit(one, &ctl.q_empty);
+          }
         }
       }
     }
-    if (!ok) {  // the tensor memory goes back only when no product runs
-      mma_commit(one, &ctl.drain);
-      const uint64_t since = global_timer_ns();
-      while (!mbar_try_wait(&ctl.drain, 0) && global_timer_ns() - since < kWaitTimeoutNs) {
-      }
+    // the tensor memory goes back only when no product runs
+    mma_commit(one, &ctl.drain);
+    const uint64_t since = global_timer_ns();
+    while (!mbar_try_wait(&ctl.drain, 0) && global_timer_ns() - since < kWaitTimeoutNs) {
     }
-  } else if (nt > 0 && warp < kSoftWarps) {
+  } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int s = warp >> 2, r = (warp & 3) * 32 + lane;  // stream, row of the query tile
-    const int tok = r / G + (PAIR ? s * TQ : 0);          // token within the CTA
-    const int h = g * G + r % G;
-    const bool valid = r < G * TQ && tok < tokens;
-    const bool active = __any_sync(0xffffffffu, valid);
-    const int end = valid ? (a.causal ? L - n + tok0 + tok + 1 : L) : 0;  // visible: t < end
     const float c = a.scale * kLog2e;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t to = tmem + lanes + 4 * kKeys + s * D;
-    const int steps = PAIR ? (s < q_tiles ? nt : 0) : (nt - s + 1) / 2;
-    float m = -INFINITY, l = 0.f;
+    const uint32_t ts = tmem + lanes + s * kKeys, to = tmem + lanes + 2 * kKeys + s * D;
+    uint32_t turn = 0, soft_turn = 0;  // parities of the stream's next scores, of the sync below
+    int mark = 0;                      // page marks of the item's first key tile
     bool ok = true;
-    for (int k = 0; k < steps; ++k) {
-      const int j = PAIR ? k : 2 * k + s;
-      ok = wait_bar(&ctl.s_full[s][k & 1], (k >> 1) & 1, &ctl.abort);
+    auto soft_sync = [&]() {  // all softmax warps; with a limit, unlike a named barrier
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.soft);
+      ok = wait_bar(&ctl.soft, soft_turn, &ctl.abort) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      soft_turn ^= 1u;
+    };
+    Take take;
+    while (ok) {
+      int steps, end;
+      bool active;
+      {
+        Work w;
+        ok = take.get(ctl, w);
+        if (!ok || w.token < 0) break;
+        const int tok = r / G + (PAIR ? s * TQ : 0);
+        const bool valid = r < G * TQ && tok < w.tokens;
+        active = __any_sync(0xffffffffu, valid);
+        steps = PAIR ? (s == 0 || w.tokens > TQ ? w.nt : 0) : (w.nt - s + 1) / 2;
+        end = (valid ? (a.causal ? w.seen + tok : w.len) : 0) - w.t0 * kKeys;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < steps; ++k) {
+        const int j = PAIR ? k : 2 * k + s;
+        ok = wait_bar(&ctl.s_full[s], turn, &ctl.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        turn ^= 1u;
+        tmem_fence_after();
+        if (active) {
+          uint32_t v[kKeys];
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 64) tmem_load64(ts + i, v + i);
+          const int lim = end - j * kKeys;
+          const uint32_t bad = ctl.bad[(mark + j) % kBadRing];
+          if (lim < kKeys) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+              if (i >= lim) v[i] = 0xff800000u;
+          }
+          if (bad != 0u) {
+            const int sh = __ffs(a.kv.bs) - 1;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i)
+              if ((bad >> (i >> sh)) & 1u) v[i] = 0xff800000u;
+          }
+          float mx[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 2)
+            mx[(i >> 1) & 7] = max3_nan(mx[(i >> 1) & 7], __uint_as_float(v[i]),
+                                        __uint_as_float(v[i + 1]));
+          const float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]),
+                                     max3_nan(mx[6], mx[7], -INFINITY));
+          if (!(top < INFINITY)) l = NAN;  // a NaN or infinite score: so is the row's softmax
+          if (k == 0) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, (top - m) * c > kRescale)) {
+            const float up = fmaxf(m, top);
+            const float f = up == -INFINITY ? 1.f : fast_exp2((m - up) * c);
+            m = up;
+            l *= f;
+            // (the scores' product was issued behind the last one into O, so that one is done)
+#pragma unroll
+            for (int i = 0; i < D; i += 32) {
+              uint32_t o[32];
+              tmem_load32(to + i, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_store32(to + i, o);
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : m * c;
+          const uint64_t cc = f32x2(c, c), mm = f32x2(-ms, -ms);
+          uint64_t sum[2] = {0, 0};
+          uint32_t x[16];
+          // a pair's scale, exponential, and sum and rounding run staggered, so that the
+          // exponential unit (8 cycles a warp instruction) does not wait for them
+#pragma unroll
+          for (int e = 0; e < kKeys / 2 + kLag; ++e) {
+            if (e < kKeys / 2) {
+              float x0, x1;
+              f32x2_split(fma2(f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                               cc, mm), x0, x1);
+              v[2 * e] = __float_as_uint(x0);
+              v[2 * e + 1] = __float_as_uint(x1);
+            }
+            if (e >= kLead && e - kLead < kKeys / 2) {
+              exp2_in_place(v[2 * (e - kLead)]);
+              exp2_in_place(v[2 * (e - kLead) + 1]);
+            }
+            if (e >= kLag) {
+              const int d = e - kLag;
+              const float p0 = __uint_as_float(v[2 * d]), p1 = __uint_as_float(v[2 * d + 1]);
+              sum[d & 1] = add2(sum[d & 1], f32x2(p0, p1));
+              x[d & 15] = pack_bf16x2(p0, p1);
+              if ((d & 15) == 15) tmem_store16(ts + (d & ~15), x);
+              if (d == kKeys / 4 - 1) {  // the first half of the weights: their products may start
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_half[s]);
+              }
+            }
+          }
+          float l0, l1;
+          f32x2_split(add2(sum[0], sum[1]), l0, l1);
+          l += l0 + l1;
+          tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(&ctl.p_half[s]);
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_full[s]);
+      }
+      if (!ok) break;
+      // -------------------------------------------------------- output
+      const Work &w = ctl.work[take.at];
+      mark = (mark + w.nt) % kBadRing;
+      const int tok = r / G + (PAIR ? s * TQ : 0), h = w.g * G + r % G;
+      const bool valid = r < G * TQ && tok < w.tokens;
+      const long long at = (static_cast<long long>(w.token) + tok) * a.Hq + h;
+      float f0 = 1.f, f1 = 0.f;
+      bool has0 = steps > 0, has1 = false;
+      // every step's product arrives on o_done: the last one's parity is behind `turn`
+      if (steps > 0) ok = wait_bar(&ctl.o_done[s], turn ^ 1u, &ctl.abort);
+      if (!PAIR) {  // join the streams: each half of the warps writes half of the dims
+        ctl.ml[s][r] = make_float2(m, l);
+        tmem_fence_before();
+        soft_sync();
+        if (!ok) break;
+        const float2 y = ctl.ml[s ^ 1][r];
+        has1 = w.nt > (s ^ 1);
+        const float both = fmaxf(m, y.x);
+        f0 = m == -INFINITY ? 0.f : fast_exp2((m - both) * c);
+        f1 = y.x == -INFINITY ? 0.f : fast_exp2((y.x - both) * c);
+        l = l * f0 + y.y * f1;
+        m = both;
+      }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tmem_fence_after();
-      if (active) {
-        const uint32_t ts = tmem + lanes + s * 2 * kKeys + (k & 1) * kKeys;
-        uint32_t v[kKeys];
-        tmem_load64(ts, v);
-        const int lim = end - (t0 + j) * kKeys;
-        const uint32_t bad = ctl.bad[j % kBadRing];
-        if (lim < kKeys) {
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-            if (i >= lim) v[i] = 0xff800000u;
-        }
-        if (bad != 0u) {
-          const int sh = __ffs(a.kv.bs) - 1;
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-            if ((bad >> (i >> sh)) & 1u) v[i] = 0xff800000u;
-        }
-        float mx[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kKeys; i += 2)
-          mx[(i >> 1) & 7] = max3_nan(mx[(i >> 1) & 7], __uint_as_float(v[i]),
-                                      __uint_as_float(v[i + 1]));
-        const float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]),
-                                   max3_nan(mx[6], mx[7], -INFINITY));
-        if (!(top < INFINITY)) l = NAN;  // a NaN or infinite score: so is the row's softmax
-        if (k == 0) {
-          m = top;
-        } else if (__any_sync(0xffffffffu, (top - m) * c > kRescale)) {
-          const float up = fmaxf(m, top);
-          const float f = up == -INFINITY ? 1.f : fast_exp2((m - up) * c);
-          m = up;
-          l *= f;
-          // the product of the step before has to be in O first
-          ok = wait_bar(&ctl.o_done[s][(k - 1) & 1], ((k - 1) >> 1) & 1, &ctl.abort);
-          tmem_fence_after();
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < D; i += 32) {
-            uint32_t o[32];
-            tmem_load32(to + i, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_store32(to + i, o);
-          }
-        }
-        const float ms = m == -INFINITY ? 0.f : m * c;
-        const uint64_t cc = f32x2(c, c), mm = f32x2(-ms, -ms);
-        uint64_t sum[2] = {0, 0};
-        uint32_t w[kKeys / 2];
-        // pair e's scale, exponential, and sum and rounding run staggered, so that the
-        // exponential unit (8 cycles a warp instruction, what bounds this loop) never waits
-#pragma unroll
-        for (int e = 0; e < kKeys / 2 + kLag; ++e) {
-          if (e < kKeys / 2) {
-            float x0, x1;
-            f32x2_split(fma2(f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), cc,
-                             mm), x0, x1);
-            v[2 * e] = __float_as_uint(x0);
-            v[2 * e + 1] = __float_as_uint(x1);
-          }
-          if (e >= kLead && e - kLead < kKeys / 2) {
-            exp2_in_place(v[2 * (e - kLead)]);
-            exp2_in_place(v[2 * (e - kLead) + 1]);
-          }
-          if (e >= kLag) {
-            const int d = e - kLag;
-            const float p0 = __uint_as_float(v[2 * d]), p1 = __uint_as_float(v[2 * d + 1]);
-            sum[d & 1] = add2(sum[d & 1], f32x2(p0, p1));
-            w[d] = pack_bf16x2(p0, p1);
-            if ((d & 15) == 15) tmem_store16(ts + (d & ~15), w + (d & ~15));
-          }
-        }
-        float l0, l1;
-        f32x2_split(add2(sum[0], sum[1]), l0, l1);
-        l += l0 + l1;
-        tmem_wait_st();
-      }
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.p_full[s][k & 1]);
-    }
-    // -------------------------------------------------------- output
-    // all products of a stream are in once its last one is
-    if (PAIR) {
-      if (steps > 0)
-        ok = ok && wait_bar(&ctl.o_done[s][(steps - 1) & 1], ((steps - 1) >> 1) & 1, &ctl.abort);
-    } else {
-      for (int i = 0; i < min(nt, 2); ++i) {
-        const int last = (nt - i + 1) / 2 - 1;
-        ok = ok && wait_bar(&ctl.o_done[i][last & 1], (last >> 1) & 1, &ctl.abort);
-      }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    tmem_fence_after();
-    float f0 = 1.f, f1 = 0.f;
-    if (!PAIR) {  // join the streams: each half of the warps writes half of the dims
-      float2 *ml = reinterpret_cast<float2 *>(tiles);  // the products have read Q
-      ml[s * kQ + r] = make_float2(m, l);
-      asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
-      const float2 x0 = ml[r], x1 = ml[kQ + r];
-      m = fmaxf(x0.x, x1.x);
-      f0 = x0.x == -INFINITY ? 0.f : fast_exp2((x0.x - m) * c);
-      f1 = x1.x == -INFINITY ? 0.f : fast_exp2((x1.x - m) * c);
-      l = x0.y * f0 + x1.y * f1;
-    }
-    if (active && ok && (steps > 0 || !PAIR)) {
-      constexpr int kCols = PAIR ? D : D / 2;
+      const bool split = w.parts > 1;
+      constexpr int kCols = PAIR ? D : D / 2;  // of this warp
       const int col0 = PAIR ? 0 : s * kCols;
-      const uint32_t o0 = tmem + lanes + 4 * kKeys + (PAIR ? s * D : 0) + col0;
-      const long long at = (static_cast<long long>(s0) + tok0 + tok) * a.Hq + h;
-      const int row = PAIR ? s * kQ + r : r;
-      float *part = p.part + (static_cast<size_t>(slot * a.Hkv + g) * p.splits + z) *
-                                 (C::kRows * (D + 2));
-      const float inv = parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      float *part = p.part + static_cast<size_t>(w.slot + w.z) * (C::kRows * (D + 2));
+      const int row = (PAIR ? s * kQ : 0) + r;
+      const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;
       f0 *= inv;
       f1 *= inv;
-      if (valid && (PAIR || s == 0)) {
-        if (parts > 1)
+      if (valid && col0 == 0) {
+        if (split)
           reinterpret_cast<float2 *>(part)[row] = make_float2(m, l);
         else if (a.lse != nullptr)
           a.lse[at] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
       }
+      if (active) {
 #pragma unroll
-      for (int i = 0; i < kCols; i += 32) {
-        uint32_t v[32];
-        tmem_load32(o0 + i, v);
-        float o[32];
+        for (int i = 0; i < kCols; i += 32) {
+          uint32_t v[32];
+          float o[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * f0;
-        if (!PAIR && nt > 1) {
-          tmem_load32(o0 + D + i, v);
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          if (has0) {
+            tmem_load32(to + col0 + i, v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(v[e]) * f1;
-        }
-        if (!valid) continue;
-        if (parts > 1) {
-          float4 *dst = reinterpret_cast<float4 *>(part + 2 * C::kRows + row * D + col0 + i);
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * f0;
+          }
+          if (has1) {
+            tmem_load32(tmem + lanes + 2 * kKeys + (s ^ 1) * D + col0 + i, v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + col0 + i);
+            for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(v[e]) * f1;
+          }
+          if (!valid) continue;
+          if (split) {
+            // [dims / 4][rows][4]: a warp's rows are neighbours
+            float4 *dst = reinterpret_cast<float4 *>(part + 2 * C::kRows) +
+                          (col0 + i) / 4 * C::kRows + row;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
-                                pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
-                                pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+            for (int e = 0; e < 8; ++e)
+              dst[e * C::kRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint16_t *dst = a.out + at * D + col0 + i;
+            uint32_t x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+            if (p.wide_out) {  // a lane's whole sectors: half the store instructions' cycles
+              store_32(dst, x);
+              store_32(dst + 16, x + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                reinterpret_cast<uint4 *>(dst)[e] =
+                    make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+          }
         }
       }
+      tmem_fence_before();
+      if (split) {
+        __threadfence();
+        soft_sync();
+        if (!ok) break;
+        if (tid == 0) {
+          ctl.last = atomicAdd(p.sem + w.slot, 1u) == static_cast<uint32_t>(w.parts) - 1u;
+          if (ctl.last) p.sem[w.slot] = 0u;
+        }
+        soft_sync();
+        if (!ok) break;
+        if (ctl.last) {
+          __threadfence();
+          join_stats<D, PAIR>(p, w, &ctl.ml[0][0], TQ, G, c);
+          soft_sync();
+          if (!ok) break;
+          join_outputs<D, PAIR>(p, w, &ctl.ml[0][0], TQ, G, c);
+          soft_sync();  // before the statistics' place is used again
+          if (!ok) break;
+        }
+      }
+      if (!PAIR) soft_sync();  // the next item's products may overwrite both streams' O
+      take.release(ctl);
     }
     tmem_fence_before();
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
 
-  if (nt > 0) {
-    __syncthreads();
-    if (warp == kSoftWarps) {
-      tmem_fence_after();
-      tmem_dealloc(tmem, 512);
-    }
-    if (ctl.abort != 0) {
-      if (tid == 0) flag_status(a.status, KSA_FLAG_WAIT_TIMEOUT);
-      return;
-    }
-  } else {  // the CTA's queries see nothing
-    for (int e = tid; e < tokens * G * (D / 8); e += kThreads) {
-      const int row = e / (D / 8);
-      const long long at =
-          (static_cast<long long>(s0) + tok0 + row / G) * a.Hq + g * G + row % G;
-      reinterpret_cast<uint4 *>(a.out + at * D)[e % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
-      if (e % (D / 8) == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
-    }
-    return;
-  }
-  if (parts == 1) return;
-
-  // ---------------------------------------------------------- join of the parts
-  uint32_t *sem = p.sem + slot * a.Hkv + g;
-  if (tid == 0) {
-    __threadfence();
-    ctl.last = atomicAdd(sem, 1u) == static_cast<uint32_t>(parts) - 1u;
-    if (ctl.last) *sem = 0u;
-  }
   __syncthreads();
-  if (!ctl.last) return;
-  __threadfence();
-  const float c = a.scale * kLog2e;
-  const size_t pitch = C::kRows * (D + 2);
-  const float *base = p.part + static_cast<size_t>(slot * a.Hkv + g) * p.splits * pitch;
-  for (int e = tid; e < tokens * G * (D / 8); e += kThreads) {
-    const int rr = e / (D / 8), d = (e % (D / 8)) * 8, tok = rr / G, hh = rr % G;
-    const int row = (PAIR ? (tok / TQ) * kQ + (tok % TQ) * G : tok * G) + hh;
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    for (int q = 0; q < parts; ++q) m = fmaxf(m, __ldcg(base + q * pitch + 2 * row));
-    for (int q = 0; q < parts; ++q) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2 *>(base + q * pitch) + row);
-      if (ml.x == -INFINITY) continue;
-      const float f = fast_exp2((ml.x - m) * c);
-      l += ml.y * f;
-      const float4 *src =
-          reinterpret_cast<const float4 *>(base + q * pitch + 2 * C::kRows + row * D + d);
-      const float4 x = __ldcg(src), y = __ldcg(src + 1);
-      o[0] += x.x * f;
-      o[1] += x.y * f;
-      o[2] += x.z * f;
-      o[3] += x.w * f;
-      o[4] += y.x * f;
-      o[5] += y.y * f;
-      o[6] += y.z * f;
-      o[7] += y.w * f;
+  if (warp == kMmaWarp) {
+    tmem_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0) {
+    if (ctl.abort != 0) {
+      flag_status(a.status, KSA_FLAG_WAIT_TIMEOUT);
+    } else if (atomicAdd(p.done, 1u) == gridDim.x - 1u) {  // every CTA has drawn its last item
+      *p.next = 0u;
+      *p.done = 0u;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const long long at = (static_cast<long long>(s0) + tok0 + tok) * a.Hq + g * G + hh;
-    *reinterpret_cast<uint4 *>(a.out + at * D + d) =
-        make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
-                   pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
-    if (d == 0 && a.lse != nullptr) a.lse[at] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
   }
 }
 
-// Two query tiles per CTA where the rows of an average sequence fill more than
-// one; the keys split where the tiles leave SMs idle (a part has at least two
-// key tiles).
-Plan make_plan(int B, int Hq, int Hkv, int D, int T, int N, int num_sms) {
-  const int G = Hq / Hkv, TQ = kQ / G;
-  Plan pl;
-  pl.pair = static_cast<long long>(N) * G > static_cast<long long>(kQ) * B;
-  pl.tokens = pl.pair ? 2 * TQ : TQ;
-  pl.slots = N / pl.tokens + B;
-  const long long items = static_cast<long long>(pl.slots) * Hkv;
-  long long splits = items > 0 ? num_sms / items : 1;
-  const int most = (T + 4 * kKeys - 1) / (4 * kKeys);
-  if (splits > most) splits = most;
-  pl.splits = splits < 1 ? 1 : static_cast<int>(splits);
-  return pl;
-}
-
-size_t sem_bytes(const Plan &pl, int Hkv) {
-  return (static_cast<size_t>(pl.slots) * Hkv * 4 + 255) / 256 * 256;
+// Two query tiles per CTA where the rows of an average sequence fill more than one.
+bool use_pairs(int B, int Hq, int Hkv, int N) {
+  return static_cast<long long>(N) * (Hq / Hkv) > static_cast<long long>(kQ) * B;
 }
 
 template <int D, bool PAIR>
-cudaError_t launch(const Params &p, const CUtensorMap *maps, cudaStream_t stream) {
+cudaError_t launch(const Params &p, const CUtensorMap *maps, int num_sms, cudaStream_t stream) {
   int occ = 0;
   auto kernel = chunk_attn_kernel<D, PAIR>;
   const cudaError_t err = kernel_occupancy(reinterpret_cast<const void *>(kernel), kThreads,
                                            Cfg<D, PAIR>::kSmem, &occ);
   if (err != cudaSuccess) return err;
-  const dim3 grid(static_cast<unsigned>(p.slots) * p.a.Hkv * p.splits);
-  kernel<<<grid, kThreads, Cfg<D, PAIR>::kSmem, stream>>>(maps[0], maps[1], maps[2], p);
+  kernel<<<num_sms, kThreads, Cfg<D, PAIR>::kSmem, stream>>>(maps[0], maps[1], maps[2], p);
   return cudaGetLastError();
 }
 
+size_t sem_bytes(int max_parts) { return (256 + static_cast<size_t>(max_parts) * 4 + 255) / 256 * 256; }
+
 }  // namespace
 
-size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int N, int num_sms) {
-  const Plan pl = make_plan(B, Hq, Hkv, D, T, N, num_sms);
-  const size_t rows = (pl.pair ? 2 : 1) * kQ;
-  const size_t parts = pl.splits == 1 ? 0
-                                      : static_cast<size_t>(pl.slots) * Hkv * pl.splits * rows *
-                                            (D + 2) * 4;
-  return sem_bytes(pl, Hkv) + (parts + 255) / 256 * 256;
+// workspace: [0] items handed out, [1] CTAs ended, from byte 256 the parts' semaphores (all zero
+// between calls), then the parts
+size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int N, int num_sms) {
+  const int max_parts = kPartsPerSm * num_sms;
+  const size_t rows = (use_pairs(B, Hq, Hkv, N) ? 2 : 1) * kQ;
+  return sem_bytes(max_parts) + static_cast<size_t>(max_parts) * rows * (D + 2) * 4;
 }
 
 cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStream_t stream) {
-  const Plan pl = make_plan(a.B, a.Hq, a.Hkv, a.D, a.T, a.N, num_sms);
   Params p;
   p.a = a;
-  p.sem = static_cast<uint32_t *>(ws);
-  p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + sem_bytes(pl, a.Hkv));
+  p.max_parts = kPartsPerSm * num_sms;
+  p.next = static_cast<uint32_t *>(ws);
+  p.done = p.next + 1;
+  p.sem = p.next + 64;
+  p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + sem_bytes(p.max_parts));
   p.tq = kQ / (a.Hq / a.Hkv);
-  p.slots = pl.slots;
-  p.splits = pl.splits;
+  p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   const bool paged = a.kv.table != nullptr;
   const uint64_t rows = paged ? static_cast<uint64_t>(a.kv.num_pages) * a.Hkv * a.kv.bs
                               : static_cast<uint64_t>(a.B) * a.Hkv * a.T;
@@ -662,9 +1031,12 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStr
       !encode_kv_tensor_map(&maps[1], a.K, rows, a.D, box) ||
       !encode_kv_tensor_map(&maps[2], a.V, rows, a.D, box))
     return cudaErrorInvalidValue;
+  const bool pair = use_pairs(a.B, a.Hq, a.Hkv, a.N);
   if (a.D == 128)
-    return pl.pair ? launch<128, true>(p, maps, stream) : launch<128, false>(p, maps, stream);
-  return pl.pair ? launch<64, true>(p, maps, stream) : launch<64, false>(p, maps, stream);
+    return pair ? launch<128, true>(p, maps, num_sms, stream)
+                : launch<128, false>(p, maps, num_sms, stream);
+  return pair ? launch<64, true>(p, maps, num_sms, stream)
+              : launch<64, false>(p, maps, num_sms, stream);
 }
 
 }  // namespace ksa
