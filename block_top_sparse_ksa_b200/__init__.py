@@ -771,34 +771,65 @@ def ksa_select_tokens_one_head(q: torch.Tensor, K: torch.Tensor, seq_lens: torch
 # paged serving: page assignment, rotary cache writes, attention of query chunks
 
 
-def _same_device(first: torch.Tensor, *others) -> None:
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+# These calls are made several times per layer and step, some of them for a few microseconds of
+# GPU work, so an argument is checked in one expression and looked at closely only if that fails.
 
 
-def _sized(t: torch.Tensor, name: str, shape) -> None:
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
-def _run_on(t: torch.Tensor, stream, fn, *args) -> None:
-    """One library call on t's device, on `stream` or that device's current stream."""
-    if t.device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
-    else:
-        with torch.cuda.device(t.device):
-            _check(fn(*args, _stream(stream)))
+def _reject(t, name: str, dtype, shape, dev: int):
+    _dev(t, name, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"tensors on different devices: {name} is on {t.device}, not cuda:{dev}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _scratch(ws: Optional[torch.Tensor], need: int, like: torch.Tensor) -> torch.Tensor:
+def _arg(t, name: str, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of that type and shape on device `dev`."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and
+                t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _reject(t, name, dtype, shape, dev)
+
+
+def _extra(t, dev: int):
+    """The address of an optional status word."""
+    if t is None:
+        return None
+    if _device_of(t, "dev_status") != dev:
+        raise ValueError(f"dev_status is on {t.device}, not cuda:{dev}")
+    return t.data_ptr()
+
+
+def _scratch(ws: Optional[torch.Tensor], need: int, dev: int):
+    """The caller's workspace as given (the library checks its size), or a fresh one of `need`
+    bytes; with its address and size."""
     if ws is None:
-        ws = torch.empty((max(int(need), 256),), dtype=torch.uint8, device=like.device)
+        ws = torch.empty((max(int(need), 256),), dtype=torch.uint8, device=f"cuda:{dev}")
         ws[:65536].zero_()  # the semaphores lie at the start; the rest needs no initial value
-        return ws
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise TypeError("workspace must be a contiguous CUDA tensor")
-    return ws
+    elif _device_of(ws, "workspace") != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _run_on(dev: int, stream, fn, *args) -> None:
+    """One library call on device `dev`, on `stream` or that device's current stream."""
+    if dev == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                    else _stream(stream))
+    if st != 0:
+        _check(st)
 
 
 def ksa_assign_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -814,43 +845,34 @@ def ksa_assign_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     [num_tokens] int64, positions [num_tokens]).  block_table [B, max_blocks] gets the new
     blocks' pages, taken off the top of the stack free_pages [num_pages]; num_free [1] is
     updated in place unless num_free_out is given.  seq_lens may be ctx_lens."""
-    _dev(ctx_lens, "ctx_lens", torch.int32)
-    _dev(new_lens, "new_lens", torch.int32)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(free_pages, "free_pages", torch.int32)
-    _dev(num_free, "num_free", torch.int32)
+    dev = _device_of(block_table, "block_table")
+    i32 = torch.int32
     B, mb = block_table.shape
-    dev = block_table.device
     if num_free_out is None:
         num_free_out = num_free
     if seq_lens is None:
-        seq_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        seq_lens = torch.empty((B,), dtype=i32, device=block_table.device)
     if cu_new is None:
-        cu_new = torch.empty((B + 1,), dtype=torch.int32, device=dev)
+        cu_new = torch.empty((B + 1,), dtype=i32, device=block_table.device)
     if slots is None:
-        slots = torch.empty((num_tokens,), dtype=torch.int64, device=dev)
+        slots = torch.empty((num_tokens,), dtype=torch.int64, device=block_table.device)
     if positions is None:
-        positions = torch.empty((num_tokens,), dtype=torch.int32, device=dev)
-    _dev(num_free_out, "num_free_out", torch.int32)
-    _dev(seq_lens, "seq_lens", torch.int32)
-    _dev(cu_new, "cu_new", torch.int32)
-    _dev(slots, "slots", torch.int64)
-    _dev(positions, "positions", torch.int32)
-    for t, name, shape in ((ctx_lens, "ctx_lens", (B,)), (new_lens, "new_lens", (B,)),
-                           (seq_lens, "seq_lens", (B,)), (cu_new, "cu_new", (B + 1,)),
-                           (num_free, "num_free", (1,)), (num_free_out, "num_free_out", (1,)),
-                           (slots, "slots", (num_tokens,)),
-                           (positions, "positions", (num_tokens,))):
-        _sized(t, name, shape)
-    ws = _scratch(workspace, 256, block_table)
-    _same_device(block_table, ctx_lens, new_lens, free_pages, num_free, num_free_out, seq_lens,
-                 cu_new, slots, positions, ws, dev_status)
-    sh = _shape(B, 1, 1, 64, mb * block_size, block_size)
-    _run_on(block_table, stream, lib().ksa_assign_pages, ctypes.byref(sh), _ptr(ctx_lens),
-            _ptr(new_lens), _ptr(block_table), mb, free_pages.numel(), _ptr(free_pages),
-            _ptr(num_free), _ptr(num_free_out), int(num_tokens), _ptr(seq_lens), _ptr(cu_new),
-            _ptr(slots), _ptr(positions), _ptr(ws), ws.numel() * ws.element_size(),
-            _ptr(dev_status))
+        positions = torch.empty((num_tokens,), dtype=i32, device=block_table.device)
+    pages = free_pages.numel()
+    ws, ws_ptr, ws_bytes = _scratch(workspace, 256, dev)
+    sh = Shape(B, 1, 1, 64, mb * block_size, block_size)
+    _run_on(dev, stream, lib().ksa_assign_pages, ctypes.byref(sh),
+            _arg(ctx_lens, "ctx_lens", i32, (B,), dev),
+            _arg(new_lens, "new_lens", i32, (B,), dev),
+            _arg(block_table, "block_table", i32, (B, mb), dev), mb, pages,
+            _arg(free_pages, "free_pages", i32, (pages,), dev),
+            _arg(num_free, "num_free", i32, (1,), dev),
+            _arg(num_free_out, "num_free_out", i32, (1,), dev), num_tokens,
+            _arg(seq_lens, "seq_lens", i32, (B,), dev),
+            _arg(cu_new, "cu_new", i32, (B + 1,), dev),
+            _arg(slots, "slots", torch.int64, (num_tokens,), dev),
+            _arg(positions, "positions", i32, (num_tokens,), dev), ws_ptr, ws_bytes,
+            _extra(dev_status, dev))
     return seq_lens, cu_new, slots, positions
 
 
@@ -860,21 +882,18 @@ def ksa_release_pages(seq_lens: torch.Tensor, done: torch.Tensor, block_table: t
                       dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows with done[b] != 0 give their pages back to the stack (free_pages, num_free); their
     table entries become -1 and their seq_lens 0, all in place."""
-    _dev(seq_lens, "seq_lens", torch.int32)
-    _dev(done, "done", torch.int32)
-    _dev(block_table, "block_table", torch.int32)
-    _dev(free_pages, "free_pages", torch.int32)
-    _dev(num_free, "num_free", torch.int32)
+    dev = _device_of(block_table, "block_table")
+    i32 = torch.int32
     B, mb = block_table.shape
-    _sized(seq_lens, "seq_lens", (B,))
-    _sized(done, "done", (B,))
-    _sized(num_free, "num_free", (1,))
-    ws = _scratch(workspace, 256, block_table)
-    _same_device(block_table, seq_lens, done, free_pages, num_free, ws, dev_status)
-    sh = _shape(B, 1, 1, 64, mb * block_size, block_size)
-    _run_on(block_table, stream, lib().ksa_release_pages, ctypes.byref(sh), _ptr(done),
-            _ptr(seq_lens), _ptr(block_table), mb, free_pages.numel(), _ptr(free_pages),
-            _ptr(num_free), _ptr(ws), ws.numel() * ws.element_size(), _ptr(dev_status))
+    pages = free_pages.numel()
+    ws, ws_ptr, ws_bytes = _scratch(workspace, 256, dev)
+    sh = Shape(B, 1, 1, 64, mb * block_size, block_size)
+    _run_on(dev, stream, lib().ksa_release_pages, ctypes.byref(sh),
+            _arg(done, "done", i32, (B,), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev),
+            _arg(block_table, "block_table", i32, (B, mb), dev), mb, pages,
+            _arg(free_pages, "free_pages", i32, (pages,), dev),
+            _arg(num_free, "num_free", i32, (1,), dev), ws_ptr, ws_bytes,
+            _extra(dev_status, dev))
 
 
 class Rotary:
@@ -904,21 +923,25 @@ class Rotary:
         self._ref = ctypes.byref(self._struct)
 
 
-def _token_rows(t: torch.Tensor, name: str) -> int:
+def _token_rows(t: torch.Tensor, name: str, dev: int, shape=None) -> int:
     """Checks a [N, heads, D] bf16 tensor whose heads and dims are dense; its token stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    n, s1, s2 = t.stride()
-    h, d = t.shape[1], t.shape[2]
+    n, h, d = t.shape
+    if (shape is not None and (n, h, d) != shape) or t.get_device() != dev:
+        _reject(t, name, torch.bfloat16, shape, dev) if t.is_contiguous() else None
+        raise ValueError(f"{name} must have shape {shape} and be on cuda:{dev}, got "
+                         f"{tuple(t.shape)} on {t.device}")
+    s0, s1, s2 = t.stride()
     if s2 != 1 or (h > 1 and s1 != d):
         raise ValueError(f"{name}: the heads and dims of a token must be dense")
-    if n >= 1 << 31:
+    if s0 >= 1 << 31:
         raise ValueError(f"{name}: a token stride of 2^31 elements or more")
-    return n if t.shape[0] > 1 else h * d
+    return s0 if n > 1 else h * d
 
 
 def _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged, dev_status, stream):
@@ -930,58 +953,53 @@ def _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged, dev_st
     if rotary is None and q is not None:
         raise ValueError("q needs a Rotary")
     lead = q if q is not None else k
-    qs = ks = vs = os_ = 0
-    N, D = lead.shape[0], lead.shape[-1]
+    dev = _device_of(lead, "q" if q is not None else "k")
+    N, Hq, D = lead.shape
+    qs = os_ = ks = vs = num_pages = 0
+    q_ptr = o_ptr = k_ptr = v_ptr = K_ptr = V_ptr = pos_ptr = slot_ptr = None
     if q is not None:
-        qs = _token_rows(q, "q")
+        qs = _token_rows(q, "q", dev)
+        q_ptr = q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        os_ = _token_rows(q_out, "q_out")
-        _sized(q_out, "q_out", q.shape)
+            q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+        os_ = _token_rows(q_out, "q_out", dev, (N, Hq, D))
+        o_ptr = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    Hkv, B, T, bs, num_pages = 1, 1, 1, 16, 0
+    Hkv, B, T, bs = Hq, 1, 1, 16
     if kv:
-        ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
-        _dev(K, "K", torch.bfloat16)
-        _dev(V, "V", torch.bfloat16)
-        _sized(k, "k", (N, K.shape[1], D))
-        _sized(v, "v", k.shape)
-        _sized(V, "V", K.shape)
-        Hkv = K.shape[1]
         if K.dim() != 4 or K.shape[3] != D:
             raise ValueError(f"K and V must be 4-dimensional with {D} dims a head")
+        cache = K.shape
+        B, Hkv, T, _ = cache
+        ks = _token_rows(k, "k", dev, (N, Hkv, D))
+        vs = _token_rows(v, "v", dev, (N, Hkv, D))
+        k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
+        K_ptr = _arg(K, "K", torch.bfloat16, cache, dev)
+        V_ptr = _arg(V, "V", torch.bfloat16, cache, dev)
         if paged:
-            num_pages, bs = K.shape[0], K.shape[2]
-            T = bs
-        else:
-            B, T = K.shape[0], K.shape[2]
+            num_pages, bs, B = B, T, 1
+        if q is None:
+            Hq = Hkv
         if slots is None:
             raise ValueError("slots must be given with k and v")
     if slots is not None:
-        _dev(slots, "slots", torch.int64)
-        _sized(slots, "slots", (N,))
+        slot_ptr = _arg(slots, "slots", torch.int64, (N,), dev)
+    ref = None
     if rotary is not None:
-        _dev(positions, "positions", torch.int32)
-        if positions.dim() == 1:
-            positions = positions[None]
-        _sized(positions, "positions", (rotary.num_axes, N))
-    _same_device(lead, k, v, slots, K, V, q_out, dev_status)
-    if rotary is not None:
-        _same_device(lead, positions)
-    Hq = q.shape[1] if q is not None else Hkv
-    if not kv:
-        Hkv = Hq
-    sh = _shape(B, Hq, Hkv, D, T, bs)
-    ref = rotary._ref if rotary is not None else None
-    args = (ctypes.byref(sh), N, ref, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
-            _ptr(positions) if rotary is not None else None, _ptr(slots), _ptr(q_out), os_,
-            _ptr(K), _ptr(V))
+        ref = rotary._ref
+        pos_ptr = (_arg(positions, "positions", torch.int32, (N,), dev)
+                   if rotary.num_axes == 1 and isinstance(positions, torch.Tensor) and
+                   positions.dim() == 1
+                   else _arg(positions, "positions", torch.int32, (rotary.num_axes, N), dev))
+    sh = Shape(B, Hq, Hkv, D, T, bs)
+    args = (ctypes.byref(sh), N, ref, q_ptr, qs, k_ptr, ks, v_ptr, vs, pos_ptr, slot_ptr, o_ptr,
+            os_, K_ptr, V_ptr)
     if paged:
-        _run_on(lead, stream, lib().ksa_rotary_append_kv_paged, *args, num_pages,
-                _ptr(dev_status))
+        _run_on(dev, stream, lib().ksa_rotary_append_kv_paged, *args, num_pages,
+                _extra(dev_status, dev))
     else:
-        _run_on(lead, stream, lib().ksa_rotary_append_kv, *args, _ptr(dev_status))
+        _run_on(dev, stream, lib().ksa_rotary_append_kv, *args, _extra(dev_status, dev))
     return q_out
 
 
@@ -1019,49 +1037,38 @@ def ksa_chunk_attn_workspace(B: int, Hq: int, Hkv: int, D: int, T: int, num_toke
 
 def _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse, workspace,
                 dev_status, stream):
-    qs = _token_rows(q, "q")
-    _dev(K, "K", torch.bfloat16)
-    _dev(V, "V", torch.bfloat16)
-    _dev(cu_q, "cu_q", torch.int32)
-    _dev(seq_lens, "seq_lens", torch.int32)
+    dev = _device_of(q, "q")
+    qs = _token_rows(q, "q", dev)
     N, Hq, D = q.shape
-    if K.dim() != 4 or K.shape[3] != D:
-        raise ValueError(f"K and V must be 4-dimensional with {D} dims a head")
-    _sized(V, "V", K.shape)
-    Hkv, bs = K.shape[1], 16
+    if not isinstance(K, torch.Tensor) or K.dim() != 4 or K.shape[3] != D:
+        raise ValueError(f"K and V must be 4-dimensional tensors with {D} dims a head")
+    cache = K.shape
+    B, Hkv, T, _ = cache
+    bs, pages = 16, None
     if block_table is not None:
-        _dev(block_table, "block_table", torch.int32)
+        num_pages, bs = B, T
         B, mb = block_table.shape
-        bs = K.shape[2]
         T = mb * bs
-    else:
-        B, T = K.shape[0], K.shape[2]
-    _sized(seq_lens, "seq_lens", (B,))
-    _sized(cu_q, "cu_q", (B + 1,))
+        pages = Pages(_arg(block_table, "block_table", torch.int32, (B, mb), dev), mb, num_pages)
     if out is None:
         out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=q.device)
-    _dev(out, "out", torch.bfloat16)
-    _sized(out, "out", q.shape)
-    if lse is not None:
-        _dev(lse, "lse", torch.float32)
-        _sized(lse, "lse", (N, Hq))
-    sh = _shape(B, Hq, Hkv, D, T, bs)
-    ws = workspace
-    if ws is None:
-        with torch.cuda.device(q.device):
+    sh = Shape(B, Hq, Hkv, D, T, bs)
+    need = 0
+    if workspace is None:
+        with torch.cuda.device(dev):
             need = lib().ksa_chunk_attn_workspace(ctypes.byref(sh), N)
-        ws = _scratch(None, need, q)
-    ws = _scratch(ws, 0, q)
-    _same_device(q, K, V, block_table, cu_q, seq_lens, out, lse, ws, dev_status)
-    rest = (_ptr(cu_q), _ptr(seq_lens), int(mask), float(scale), _ptr(out), _ptr(lse), _ptr(ws),
-            ws.numel() * ws.element_size(), _ptr(dev_status))
-    if block_table is not None:
-        pg = _pages(block_table, K.shape[0])
-        _run_on(q, stream, lib().ksa_chunk_attn_paged, ctypes.byref(sh), N, _ptr(q), qs, _ptr(K),
-                _ptr(V), ctypes.byref(pg), *rest)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, need, dev)
+    head = (ctypes.byref(sh), N, q.data_ptr(), qs, _arg(K, "K", torch.bfloat16, cache, dev),
+            _arg(V, "V", torch.bfloat16, cache, dev))
+    rest = (_arg(cu_q, "cu_q", torch.int32, (B + 1,), dev),
+            _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), mask, scale,
+            _arg(out, "out", torch.bfloat16, (N, Hq, D), dev),
+            None if lse is None else _arg(lse, "lse", torch.float32, (N, Hq), dev), ws_ptr,
+            ws_bytes, _extra(dev_status, dev))
+    if pages is not None:
+        _run_on(dev, stream, lib().ksa_chunk_attn_paged, *head, ctypes.byref(pages), *rest)
     else:
-        _run_on(q, stream, lib().ksa_chunk_attn, ctypes.byref(sh), N, _ptr(q), qs, _ptr(K),
-                _ptr(V), *rest)
+        _run_on(dev, stream, lib().ksa_chunk_attn, *head, *rest)
     return out, lse
 
 

@@ -480,3 +480,29 @@ def test_validation_of_chunk_attention(ksa):
     assert call(n=0, q=None) == 0
     bad = _shape(ksa, D=96)
     assert lib.ksa_chunk_attn_workspace(ctypes.byref(bad), 7) == 0
+
+
+def test_serving_calls_refuse_cpu_tensors(ksa):
+    """The tensors' type, shape and device are checked before the library is called; CPU tensors
+    are refused by name."""
+    import torch
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="block_table must be a CUDA tensor"):
+        ksa.ksa_assign_pages(i32(2), i32(2), i32(2, 4), i32(9), i32(1), 16, 3)
+    with pytest.raises(TypeError, match="block_table must be a CUDA tensor"):
+        ksa.ksa_release_pages(i32(2), i32(2), i32(2, 4), i32(9), i32(1), 16)
+    rot = ksa.Rotary([0.5] * 64)
+    with pytest.raises(TypeError, match="q must be a CUDA tensor"):
+        ksa.ksa_rotary_append_kv(bf(3, 4, 128), bf(3, 2, 128), bf(3, 2, 128), i32(3),
+                                 torch.zeros(3, dtype=torch.int64), bf(1, 2, 8, 128),
+                                 bf(1, 2, 8, 128), rot)
+    with pytest.raises(ValueError, match="together"):
+        ksa.ksa_rotary_append_kv(bf(3, 4, 128), bf(3, 2, 128), None, i32(3), None, None, None, rot)
+    with pytest.raises(ValueError, match="Rotary"):
+        ksa.ksa_rotary_append_kv(bf(3, 4, 128), None, None, i32(3), None, None, None, None)
+    with pytest.raises(TypeError, match="q must be a CUDA tensor"):
+        ksa.ksa_chunk_attn(bf(3, 4, 128), bf(1, 2, 8, 128), bf(1, 2, 8, 128), i32(2), i32(1))
+    with pytest.raises(TypeError, match="block_table must be a CUDA tensor"):
+        ksa.ksa_chunk_attn_paged(bf(3, 4, 128), bf(1, 2, 16, 128), bf(1, 2, 16, 128), None,
+                                 i32(2), i32(1))

@@ -708,3 +708,48 @@ def test_chunk_attn_captured_in_two_graphs(ksa):
             assert torch.equal(o, want)
     assert torch.equal(eager[0], out)
     del graphs
+
+
+def test_serving_calls_refuse_wrong_tensors(ksa):
+    """Type, shape, layout and device of every tensor, by name, before anything is launched."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=DEV)
+    q, K, cu, seq = bf(4, 4, 64), bf(2, 2, 32, 64), i32([0, 3, 4]), i32([5, 6])
+    ok = lambda **kw: ksa.ksa_chunk_attn(**{**dict(q=q, K=K, V=K, cu_q=cu, seq_lens=seq), **kw})
+    ok()
+    for kw, kind in ((dict(q=q.float()), TypeError), (dict(K=K.half()), TypeError),
+                     (dict(V=K[:, :, :16]), ValueError), (dict(K=K.transpose(2, 3)), ValueError),
+                     (dict(cu_q=cu[:2]), ValueError), (dict(cu_q=cu.long()), TypeError),
+                     (dict(seq_lens=seq.cpu()), TypeError), (dict(out=bf(4, 4, 32)), ValueError),
+                     (dict(out=q.float()), TypeError), (dict(lse=bf(4, 4)), TypeError),
+                     (dict(lse=torch.zeros((4, 3), device=DEV)), ValueError),
+                     (dict(q=q.transpose(0, 1)), ValueError),
+                     (dict(workspace=torch.zeros(9, dtype=torch.uint8)), TypeError),
+                     (dict(workspace=torch.zeros(256, dtype=torch.uint8, device=DEV)),
+                      ksa.KsaError)):
+        with pytest.raises(kind):
+            ok(**kw)
+    table, free, one = i32([[0, 1]]), i32([0, 1, 2]), i32([1])
+    ok = lambda **kw: ksa.ksa_assign_pages(**{**dict(
+        ctx_lens=one, new_lens=one, block_table=table, free_pages=free, num_free=one,
+        block_size=16, num_tokens=2), **kw})
+    for kw, kind in ((dict(ctx_lens=i32([1, 2])), ValueError), (dict(new_lens=one.long()), TypeError),
+                     (dict(block_table=table.T), ValueError), (dict(num_free=one.cpu()), TypeError),
+                     (dict(slots=i32([0, 0])), TypeError), (dict(block_size=8), ksa.KsaError),
+                     (dict(positions=i32([0])), ValueError), (dict(num_tokens=-1, slots=one.long(),
+                                                                   positions=one), ValueError)):
+        with pytest.raises(kind):
+            ok(**kw)
+    rot, k = ksa.Rotary([0.5] * 32), bf(4, 2, 64)
+    slots, pos = torch.arange(4, device=DEV), i32([0, 1, 2, 3])
+    ok = lambda **kw: ksa.ksa_rotary_append_kv(**{**dict(
+        q=q, k=k, v=k, positions=pos, slots=slots, K=K, V=K.clone(), rotary=rot), **kw})
+    ok()
+    for kw, kind in ((dict(k=bf(3, 2, 64)), ValueError), (dict(v=k.float()), TypeError),
+                     (dict(slots=slots.int()), TypeError), (dict(positions=pos[:3]), ValueError),
+                     (dict(positions=pos.cpu()), TypeError), (dict(positions=None), TypeError),
+                     (dict(slots=None), ValueError), (dict(q_out=bf(4, 4, 32)), ValueError),
+                     (dict(rotary=ksa.Rotary([0.5] * 32, num_axes=2)), ValueError),
+                     (dict(rotary=ksa.Rotary([0.5] * 40)), ksa.KsaError),
+                     (dict(V=K[:1]), ValueError), (dict(K=bf(2, 2, 64)), ValueError)):
+        with pytest.raises(kind):
+            ok(**kw)
