@@ -182,25 +182,35 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignArgs
       for (int r = threadIdx.x; r < rows; r += kThreads) a.cu_new[base + r] = min(c.place[r], a.N);
       if (threadIdx.x == 0 && base + kChunk >= a.B) a.cu_new[a.B] = min(tokens, a.N);
     }
-    for (int t = max(t0, before) + threadIdx.x; t < min(t1, tokens); t += kThreads) {
+    // a thread's places together: their pages' loads are in flight at once
+    const int lo = max(t0, before) + threadIdx.x, hi = min(t1, tokens);
+    int pos[kTokens / kThreads], page[kTokens / kThreads], *fresh[kTokens / kThreads];
+#pragma unroll
+    for (int i = 0; i < kTokens / kThreads; ++i) {
+      const int t = lo + i * kThreads;
+      pos[i] = page[i] = -1;
+      fresh[i] = nullptr;
+      if (t >= hi) continue;
       const int r = find_row(c, rows, t);
-      long long slot = -1;
-      int pos = -1;
-      if (c.first[r] >= 0) {
-        const int held = (c.ctx[r] + a.bs - 1) / a.bs;
-        pos = c.ctx[r] + (t - c.place[r]);
-        const int j = pos / a.bs, off = pos - j * a.bs;
-        int *entry = a.block_table + static_cast<size_t>(base + r) * a.max_blocks + j;
-        int page = j < held ? *entry : a.free_pages[F - 1 - (c.first[r] + j - held)];
-        if (page < 0 || page >= a.num_pages) {
-          flag_status(a.status, KSA_FLAG_INDEX_SKIPPED);
-          page = -1;
-        }
-        if (j >= held && off == 0) *entry = page;
-        if (page >= 0) slot = static_cast<long long>(page) * a.bs + off;
+      if (c.first[r] < 0) continue;
+      const int held = (c.ctx[r] + a.bs - 1) / a.bs;
+      pos[i] = c.ctx[r] + (t - c.place[r]);
+      const int j = pos[i] / a.bs;
+      int *entry = a.block_table + static_cast<size_t>(base + r) * a.max_blocks + j;
+      page[i] = j < held ? *entry : a.free_pages[F - 1 - (c.first[r] + j - held)];
+      if (j >= held && pos[i] == j * a.bs) fresh[i] = entry;  // the new block's first token
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens / kThreads; ++i) {
+      const int t = lo + i * kThreads;
+      if (t >= hi) continue;
+      if (pos[i] >= 0 && (page[i] < 0 || page[i] >= a.num_pages)) {
+        flag_status(a.status, KSA_FLAG_INDEX_SKIPPED);
+        page[i] = -1;
       }
-      a.slots[t] = slot;
-      a.positions[t] = pos;
+      if (fresh[i] != nullptr) *fresh[i] = page[i];
+      a.slots[t] = page[i] < 0 ? -1LL : static_cast<long long>(page[i]) * a.bs + pos[i] % a.bs;
+      a.positions[t] = pos[i];
     }
     if (base + kChunk < a.B) __syncthreads();  // the chunk is read before the next one fills it
   }
@@ -290,18 +300,27 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleaseAr
     for (long long e0 = static_cast<long long>(blockIdx.x) * kTokens; e0 < blocks;
          e0 += static_cast<long long>(gridDim.x) * kTokens) {
       const int end = static_cast<int>(min(e0 + kTokens, static_cast<long long>(blocks)));
-      for (int e = max(static_cast<int>(e0), before) + threadIdx.x; e < end; e += kThreads) {
+      const int lo = max(static_cast<int>(e0), before) + threadIdx.x;
+      int *entry[kTokens / kThreads], page[kTokens / kThreads];
+#pragma unroll
+      for (int i = 0; i < kTokens / kThreads; ++i) {
+        const int e = lo + i * kThreads;
+        entry[i] = nullptr;
+        if (e >= end) continue;
         const int r = find_row(c, rows, e);
-        int *entry = a.block_table + static_cast<size_t>(base + r) * a.max_blocks +
-                     (e - c.place[r]);
-        int page = *entry;
-        *entry = -1;
-        if (page < 0 || page >= a.num_pages) {
+        entry[i] = a.block_table + static_cast<size_t>(base + r) * a.max_blocks + (e - c.place[r]);
+        page[i] = *entry[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kTokens / kThreads; ++i) {
+        if (entry[i] == nullptr) continue;
+        *entry[i] = -1;
+        if (page[i] < 0 || page[i] >= a.num_pages) {
           flag_status(a.status, KSA_FLAG_INDEX_SKIPPED);
-          page = -1;
+          page[i] = -1;
         }
-        const int at = F + (total - 1 - e);
-        if (at < a.num_pages) a.free_pages[at] = page;
+        const int at = F + (total - 1 - (lo + i * kThreads));
+        if (at < a.num_pages) a.free_pages[at] = page[i];
       }
     }
   }

@@ -483,7 +483,7 @@ typedef struct {
  *   K[b, g, t, :]  = rotated k[n, g, :],  V[b, g, t, :] = v[n, g, :],
  * slot s = b * T + t in a contiguous cache, s = page * bs + offset in a paged
  * one (the slots of ksa_assign_pages).  A negative slot is padding: nothing of
- * the token is read or written.  A slot past the cache likewise, and it sets
+ * the token is written.  A slot past the cache likewise, and it sets
  * KSA_FLAG_INDEX_SKIPPED.  Slots must be distinct.
  *   rotary:    read before the call returns; NULL: K/V are written unrotated
  *              (encoder states), q must then be NULL
