@@ -52,7 +52,7 @@ constexpr int kCtlBytes = 3072;
 
 template <int D, bool PAIR>
 struct Cfg {
-  static constexpr int kQBytes = kQ * D * 2, kTileBytes = kKeys * D * 2;  // of a Q, of a K or V tile
+  static constexpr int kQBytes = kQ * D * 2, kTileBytes = kKeys * D * 2;  // of Q, of K or V
   static constexpr int kQTiles = PAIR ? 2 : 1;
   static constexpr int kStages = (224 * 1024 - kQTiles * kQBytes) / kTileBytes;
   static constexpr int kRows = kQ * kQTiles;      // query rows of a CTA
@@ -1000,7 +1000,9 @@ cudaError_t launch(const Params &p, const CUtensorMap *maps, int num_sms, cudaSt
   return cudaGetLastError();
 }
 
-size_t sem_bytes(int max_parts) { return (256 + static_cast<size_t>(max_parts) * 4 + 255) / 256 * 256; }
+size_t sem_bytes(int max_parts) {
+  return (256 + static_cast<size_t>(max_parts) * 4 + 255) / 256 * 256;
+}
 
 }  // namespace
 

@@ -44,6 +44,16 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 using ksa::device_sm_count;
 
+// Runs an entry point's body; nothing it throws (out of host memory) crosses the C boundary.
+template <typename Body>
+ksa_status guarded(Body body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    return KSA_ERR_CUDA;
+  }
+}
+
 ksa_status check_shape(const ksa_shape *s, bool need_block) {
   if (s == nullptr) return fail(KSA_ERR_INVALID_ARG, "shape is NULL");
   if (s->batch < 1 || s->num_q_heads < 1 || s->num_kv_heads < 1 || s->capacity < 1)
@@ -833,71 +843,75 @@ ksa_status ksa_assign_pages(const ksa_shape *shape, const int32_t *ctx_lens,
                             int32_t num_tokens, int32_t *seq_lens, int32_t *cu_new,
                             int64_t *slots, int32_t *positions, void *ws, size_t ws_bytes,
                             uint32_t *dev_status, void *stream) {
-  ksa_status st = check_page_call(shape, block_table, max_blocks, num_pages, free_pages,
-                                  num_free, ws, ws_bytes);
-  if (st != KSA_OK) return st;
-  if (ctx_lens == nullptr || new_lens == nullptr || num_free_out == nullptr ||
-      seq_lens == nullptr || cu_new == nullptr)
-    return fail(KSA_ERR_INVALID_ARG,
-                "ctx_lens, new_lens, num_free_out, seq_lens and cu_new must be non-NULL");
-  if (num_tokens < 0 || num_tokens >= (1 << 30))
-    return fail(KSA_ERR_INVALID_ARG, "num_tokens %d is not in [0, 2^30)", num_tokens);
-  if (num_tokens > 0 && (slots == nullptr || positions == nullptr))
-    return fail(KSA_ERR_INVALID_ARG, "slots and positions must be non-NULL");
-  if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(num_free_out, 4) ||
-      !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(slots, 8) ||
-      !aligned(positions, 4))
-    return fail(KSA_ERR_INVALID_ARG, "slots must be 8-byte aligned, the other arrays 4-byte");
-  ksa::AssignArgs a;
-  a.ctx_lens = ctx_lens;
-  a.new_lens = new_lens;
-  a.block_table = block_table;
-  a.free_pages = free_pages;
-  a.num_free = num_free;
-  a.num_free_out = num_free_out;
-  a.seq_lens = seq_lens;
-  a.cu_new = cu_new;
-  a.slots = slots;
-  a.positions = positions;
-  a.counter = static_cast<uint32_t *>(ws);
-  a.status = dev_status;
-  a.B = shape->batch;
-  a.T = shape->capacity;
-  a.bs = shape->block_size;
-  a.max_blocks = max_blocks;
-  a.num_pages = num_pages;
-  a.N = num_tokens;
-  return cuda_status(ksa::launch_assign_pages(a, static_cast<cudaStream_t>(stream)),
-                     "ksa_assign_pages launch");
+  return guarded([&]() -> ksa_status {
+    ksa_status st = check_page_call(shape, block_table, max_blocks, num_pages, free_pages,
+                                    num_free, ws, ws_bytes);
+    if (st != KSA_OK) return st;
+    if (ctx_lens == nullptr || new_lens == nullptr || num_free_out == nullptr ||
+        seq_lens == nullptr || cu_new == nullptr)
+      return fail(KSA_ERR_INVALID_ARG,
+                  "ctx_lens, new_lens, num_free_out, seq_lens and cu_new must be non-NULL");
+    if (num_tokens < 0 || num_tokens >= (1 << 30))
+      return fail(KSA_ERR_INVALID_ARG, "num_tokens %d is not in [0, 2^30)", num_tokens);
+    if (num_tokens > 0 && (slots == nullptr || positions == nullptr))
+      return fail(KSA_ERR_INVALID_ARG, "slots and positions must be non-NULL");
+    if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(num_free_out, 4) ||
+        !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(slots, 8) ||
+        !aligned(positions, 4))
+      return fail(KSA_ERR_INVALID_ARG, "slots must be 8-byte aligned, the other arrays 4-byte");
+    ksa::AssignArgs a;
+    a.ctx_lens = ctx_lens;
+    a.new_lens = new_lens;
+    a.block_table = block_table;
+    a.free_pages = free_pages;
+    a.num_free = num_free;
+    a.num_free_out = num_free_out;
+    a.seq_lens = seq_lens;
+    a.cu_new = cu_new;
+    a.slots = slots;
+    a.positions = positions;
+    a.counter = static_cast<uint32_t *>(ws);
+    a.status = dev_status;
+    a.B = shape->batch;
+    a.T = shape->capacity;
+    a.bs = shape->block_size;
+    a.max_blocks = max_blocks;
+    a.num_pages = num_pages;
+    a.N = num_tokens;
+    return cuda_status(ksa::launch_assign_pages(a, static_cast<cudaStream_t>(stream)),
+                       "ksa_assign_pages launch");
+  });
 }
 
 ksa_status ksa_release_pages(const ksa_shape *shape, const int32_t *done, int32_t *seq_lens,
                              int32_t *block_table, int32_t max_blocks, int32_t num_pages,
                              int32_t *free_pages, int32_t *num_free, void *ws,
                              size_t ws_bytes, uint32_t *dev_status, void *stream) {
-  ksa_status st = check_page_call(shape, block_table, max_blocks, num_pages, free_pages,
-                                  num_free, ws, ws_bytes);
-  if (st != KSA_OK) return st;
-  if (done == nullptr || seq_lens == nullptr)
-    return fail(KSA_ERR_INVALID_ARG, "done and seq_lens must be non-NULL");
-  if (!aligned(done, 4) || !aligned(seq_lens, 4))
-    return fail(KSA_ERR_INVALID_ARG, "done and seq_lens must be 4-byte aligned");
-  ksa::ReleaseArgs a;
-  a.done = done;
-  a.seq_lens = seq_lens;
-  a.block_table = block_table;
-  a.free_pages = free_pages;
-  a.num_free = num_free;
-  a.counter = static_cast<uint32_t *>(ws);
-  a.status = dev_status;
-  a.B = shape->batch;
-  a.T = shape->capacity;
-  a.bs = shape->block_size;
-  a.max_blocks = max_blocks;
-  a.num_pages = num_pages;
-  return cuda_status(
-      ksa::launch_release_pages(a, device_sm_count(), static_cast<cudaStream_t>(stream)),
-      "ksa_release_pages launch");
+  return guarded([&]() -> ksa_status {
+    ksa_status st = check_page_call(shape, block_table, max_blocks, num_pages, free_pages,
+                                    num_free, ws, ws_bytes);
+    if (st != KSA_OK) return st;
+    if (done == nullptr || seq_lens == nullptr)
+      return fail(KSA_ERR_INVALID_ARG, "done and seq_lens must be non-NULL");
+    if (!aligned(done, 4) || !aligned(seq_lens, 4))
+      return fail(KSA_ERR_INVALID_ARG, "done and seq_lens must be 4-byte aligned");
+    ksa::ReleaseArgs a;
+    a.done = done;
+    a.seq_lens = seq_lens;
+    a.block_table = block_table;
+    a.free_pages = free_pages;
+    a.num_free = num_free;
+    a.counter = static_cast<uint32_t *>(ws);
+    a.status = dev_status;
+    a.B = shape->batch;
+    a.T = shape->capacity;
+    a.bs = shape->block_size;
+    a.max_blocks = max_blocks;
+    a.num_pages = num_pages;
+    return cuda_status(
+        ksa::launch_release_pages(a, device_sm_count(), static_cast<cudaStream_t>(stream)),
+        "ksa_release_pages launch");
+  });
 }
 
 namespace {
@@ -1012,9 +1026,11 @@ ksa_status ksa_rotary_append_kv(const ksa_shape *shape, int32_t num_tokens,
                                 int32_t v_stride, const int32_t *positions,
                                 const int64_t *slots, uint16_t *q_out, int32_t q_out_stride,
                                 uint16_t *K, uint16_t *V, uint32_t *dev_status, void *stream) {
-  return rotary_common(shape, num_tokens, rotary, q, q_stride, k, k_stride, v, v_stride,
-                       positions, slots, q_out, q_out_stride, K, V, false, 0, dev_status,
-                       stream);
+  return guarded([&]() -> ksa_status {
+    return rotary_common(shape, num_tokens, rotary, q, q_stride, k, k_stride, v, v_stride,
+                         positions, slots, q_out, q_out_stride, K, V, false, 0, dev_status,
+                         stream);
+  });
 }
 
 ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens,
@@ -1025,9 +1041,11 @@ ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens
                                       uint16_t *q_out, int32_t q_out_stride,
                                       uint16_t *K_pages, uint16_t *V_pages, int32_t num_pages,
                                       uint32_t *dev_status, void *stream) {
-  return rotary_common(shape, num_tokens, rotary, q, q_stride, k, k_stride, v, v_stride,
-                       positions, slots, q_out, q_out_stride, K_pages, V_pages, true, num_pages,
-                       dev_status, stream);
+  return guarded([&]() -> ksa_status {
+    return rotary_common(shape, num_tokens, rotary, q, q_stride, k, k_stride, v, v_stride,
+                         positions, slots, q_out, q_out_stride, K_pages, V_pages, true, num_pages,
+                         dev_status, stream);
+  });
 }
 
 namespace {
@@ -1112,8 +1130,10 @@ ksa_status ksa_chunk_attn(const ksa_shape *shape, int32_t num_tokens, const uint
                           const int32_t *cu_q, const int32_t *seq_lens, int32_t mask,
                           float scale, uint16_t *out, float *lse, void *ws, size_t ws_bytes,
                           uint32_t *dev_status, void *stream) {
-  return chunk_common(shape, num_tokens, q, q_stride, K, V, nullptr, false, cu_q, seq_lens, mask,
-                      scale, out, lse, ws, ws_bytes, dev_status, stream);
+  return guarded([&]() -> ksa_status {
+    return chunk_common(shape, num_tokens, q, q_stride, K, V, nullptr, false, cu_q, seq_lens, mask,
+                        scale, out, lse, ws, ws_bytes, dev_status, stream);
+  });
 }
 
 ksa_status ksa_chunk_attn_paged(const ksa_shape *shape, int32_t num_tokens, const uint16_t *q,
@@ -1122,8 +1142,10 @@ ksa_status ksa_chunk_attn_paged(const ksa_shape *shape, int32_t num_tokens, cons
                                 const int32_t *cu_q, const int32_t *seq_lens, int32_t mask,
                                 float scale, uint16_t *out, float *lse, void *ws,
                                 size_t ws_bytes, uint32_t *dev_status, void *stream) {
-  return chunk_common(shape, num_tokens, q, q_stride, K_pages, V_pages, pages, true, cu_q,
-                      seq_lens, mask, scale, out, lse, ws, ws_bytes, dev_status, stream);
+  return guarded([&]() -> ksa_status {
+    return chunk_common(shape, num_tokens, q, q_stride, K_pages, V_pages, pages, true, cu_q,
+                        seq_lens, mask, scale, out, lse, ws, ws_bytes, dev_status, stream);
+  });
 }
 
 ksa_status ksa_get_device_status(const uint32_t *dev_status, void *stream, int32_t clear,

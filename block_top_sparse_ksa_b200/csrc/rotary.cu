@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 }  // namespace
 
 cudaError_t launch_rotary_append(const RotaryArgs &a, int num_sms, cudaStream_t stream) {
-  // as many tokens per CTA as its threads take in kRounds rounds; fewer while that leaves SMs without
-  // work, so that a decode step's tokens spread
+  // as many tokens per CTA as its threads take in kRounds rounds; fewer while that leaves SMs
+  // without work, so that a decode step's tokens spread
   const int heads = (a.q != nullptr ? a.Hq : 0) + (a.k != nullptr ? 2 * a.Hkv : 0);
   int tok = kRounds * kThreads * kUnroll / (heads * (a.D / 16));
   const int spread = a.N / (4 * num_sms);
@@ -171,7 +171,8 @@ cudaError_t launch_rotary_append(const RotaryArgs &a, int num_sms, cudaStream_t 
   // x / heads = umulhi(x, per_head) for the x < tok * heads of more than one token, since then
   // heads <= 384: the product's error, below x * heads / 2^32, stays below 1 / heads
   const uint32_t per_head = static_cast<uint32_t>((0x100000000ull + heads - 1) / heads);
-  if (a.D == 128) return launch_pdl(rotary_append_kernel<128>, grid, block, 0, stream, a, tok, per_head);
+  if (a.D == 128)
+    return launch_pdl(rotary_append_kernel<128>, grid, block, 0, stream, a, tok, per_head);
   return launch_pdl(rotary_append_kernel<64>, grid, block, 0, stream, a, tok, per_head);
 }
 

@@ -527,10 +527,13 @@ ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens
  *   z_t = scale * <q[n,h,:], K[b,g,t,:]>,  w = softmax(z over the visible t),
  *   out[n,h,:] = sum_t w_t V[b,g,t,:],  lse[n,h] = log sum_t exp(z_t).
  * A query that sees nothing (L_b = 0, or more new tokens than cached ones)
- * gives out = 0 and lse = -inf.  What the cache holds outside the visible
- * tokens (NaN, infinities) does not matter.  Scores, the running maximum and
- * sum and the output accumulate in fp32; the weights are rounded to bf16 for
- * the product with V (relative error up to 2^-8 each), and out once to bf16.
+ * gives out = 0 and lse = -inf.  What the cache holds behind a row's L_b tokens
+ * (NaN, infinities) does not matter.  A query that sees a NaN or infinite score
+ * gets NaN; a NaN or infinity in V of a chunk's token may also reach the
+ * chunk's earlier queries (a weight of 0 times it).  Scores, the running
+ * maximum and sum and the output accumulate in fp32; the weights are rounded to
+ * bf16 for the product with V (relative error up to 2^-8 each), and out once to
+ * bf16.
  *   q:    bf16, token stride q_stride elements (a multiple of 8), heads and
  *         dims dense;  cu_q: [B+1] int32, ascending;  seq_lens: [B] int32
  *         (0 is allowed; outside [0, T] is clamped and flagged)
@@ -540,6 +543,8 @@ ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens
  * scale == 0 selects 1/sqrt(D).  Places of q and out that no row covers are
  * left alone.  Entries of cu_q outside [0, num_tokens] or descending are
  * clamped and flagged KSA_FLAG_SEQ_LEN_CLAMPED; num_tokens = 0 does nothing.
+ * One launch of one CTA per SM; the lengths are read on the device, so a
+ * captured call follows them.  The results do not depend on timing.
  * Limits: D in {64, 128}; G <= 128.
  */
 enum { KSA_MASK_NONE = 0, KSA_MASK_CAUSAL = 1 };

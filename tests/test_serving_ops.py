@@ -100,8 +100,9 @@ def page_state(rng, ctx, mb, bs, spare):
 def run_assign(ksa, ctx, new, table, free, F, bs, N, **kw):
     st = status()
     t, nf, out = torch.from_numpy(table).to(DEV), i32([F]), torch.full((1,), -7).to(DEV).int()
-    seq, cu, slots, pos = ksa.ksa_assign_pages(i32(ctx), i32(new), t, torch.from_numpy(free).to(DEV),
-                                               nf, bs, N, num_free_out=out, dev_status=st, **kw)
+    seq, cu, slots, pos = ksa.ksa_assign_pages(i32(ctx), i32(new), t,
+                                               torch.from_numpy(free).to(DEV), nf, bs, N,
+                                               num_free_out=out, dev_status=st, **kw)
     assert int(nf) == F
     return t, out, seq, cu, slots, pos, int(st)
 
@@ -317,7 +318,8 @@ def test_rotary_append(ksa, paged, N, Hq, Hkv, D, P, axes, inter, far):
     want, mag = ref_rotary(q, pos, axis, freq, inter)
     close_rotary(q_out[keep], want[real], mag[real], P)
     assert bool((q_out[~keep] == 3.0).all())
-    pg, off = torch.from_numpy(slots[real] // per).to(DEV), torch.from_numpy(slots[real] % per).to(DEV)
+    pg = torch.from_numpy(slots[real] // per).to(DEV)
+    off = torch.from_numpy(slots[real] % per).to(DEV)
     want, mag = ref_rotary(k, pos, axis, freq, inter)
     close_rotary(K[pg, :, off], want[real], mag[real], P)
     assert torch.equal(V[pg, :, off], v[keep])
@@ -732,7 +734,8 @@ def test_serving_calls_refuse_wrong_tensors(ksa):
     ok = lambda **kw: ksa.ksa_assign_pages(**{**dict(
         ctx_lens=one, new_lens=one, block_table=table, free_pages=free, num_free=one,
         block_size=16, num_tokens=2), **kw})
-    for kw, kind in ((dict(ctx_lens=i32([1, 2])), ValueError), (dict(new_lens=one.long()), TypeError),
+    for kw, kind in ((dict(ctx_lens=i32([1, 2])), ValueError),
+                     (dict(new_lens=one.long()), TypeError),
                      (dict(block_table=table.T), ValueError), (dict(num_free=one.cpu()), TypeError),
                      (dict(slots=i32([0, 0])), TypeError), (dict(block_size=8), ksa.KsaError),
                      (dict(positions=i32([0])), ValueError), (dict(num_tokens=-1, slots=one.long(),
@@ -753,3 +756,84 @@ def test_serving_calls_refuse_wrong_tensors(ksa):
                      (dict(V=K[:1]), ValueError), (dict(K=bf(2, 2, 64)), ValueError)):
         with pytest.raises(kind):
             ok(**kw)
+
+
+def test_chunk_attn_non_finite_scores(ksa):
+    """A NaN or infinite key reaches exactly the queries that see it; one behind a causal query
+    does not, and huge finite scores stay finite.  Whole and split items."""
+    n, L, D = 6, 700, 64
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for L in (700, 9000):
+            cache = Cache([L, 300], 1, D, 16, False, 12)
+            q = randn((n + 3, 2, D), 5).abs() + 0.5  # no score of an infinite key is a NaN sum
+            cache.K[0, 0, L - 3] = bad  # seen by the last three of the six queries
+            out, lse = (torch.empty((n + 3, 2, D), dtype=torch.bfloat16, device=DEV),
+                        torch.empty((n + 3, 2), device=DEV))
+            cache.call(ksa, q, i32([0, n, n + 3]), i32([L, 300]), ksa.MASK_CAUSAL, out=out,
+                       lse=lse)
+            k = cache.K[0, :, :L]
+            want, want_lse, mag = ref_attn(q[:n], k, cache.rows[0][1], n, L, True, D ** -0.5)
+            seen = torch.arange(n, device=DEV) >= n - 3
+            if bad == -float("inf"):  # weighs nothing
+                assert bool(torch.isfinite(out.float()).all())
+                seen[:] = False
+            else:
+                assert bool(out[:n][seen].isnan().all()) and bool(lse[:n][seen].isnan().all())
+            off = (out[:n].double() - want).abs() - (HALF + 4e-4) * mag - HALF * want.abs()
+            assert bool((off[~seen] <= 0).all())
+            assert float((lse[:n].double() - want_lse)[~seen].abs().max()) <= 1e-4
+            assert bool(torch.isfinite(out[n:].float()).all())
+    # scores up to 64 * 200 * 200 / 8: one weight is 1, nothing overflows
+    cache = Cache([400], 1, D, 16, True, 13)
+    q = randn((40, 4, D), 6) * 200
+    cache.K *= 200
+    lse = torch.empty((40, 4), device=DEV)
+    out, _ = cache.call(ksa, q, i32([0, 40]), i32([400]), ksa.MASK_CAUSAL, lse=lse)
+    assert bool(torch.isfinite(out.float()).all()) and bool(torch.isfinite(lse).all())
+
+
+def test_chunk_attn_many_rows_and_heads(ksa):
+    """More rows than one look-up takes, in mixed depths, some empty; items cut by the mean row."""
+    rng = np.random.default_rng(2)
+    for B, far in ((75, 900), (200, 40), (33, 5000)):
+        rows = [(int(rng.integers(0, 4)), int(rng.integers(0, far))) for _ in range(B)]
+        rows[B // 2] = (9, far)
+        check_attn(ksa, rows, 4, 2, 64, 16, B != 200, B == 75, seed=B)
+    rows = [(int(rng.integers(100, 300)), int(rng.integers(1, 3000))) for _ in range(40)]
+    check_attn(ksa, rows, 2, 1, 64, 32, True, False, seed=40)
+
+
+def test_chunk_attn_equal_items_with_a_cut_tail(ksa):
+    """Items of one depth that leave a last round half empty: whole ones, then parts."""
+    for n, Hkv in ((64 * 37, 5), (64 * 20, 8), (100, 8)):
+        check_attn(ksa, [(n, 9000)], Hkv * 4, Hkv, 64, 16, False, False, seed=n)
+
+
+def test_chunk_attn_repeats_bit_for_bit(ksa):
+    """The order in which CTAs finish does not reach the results: split and whole items, 20 runs."""
+    for rows, Hq, Hkv in (([(5, 40000)], 8, 2), ([(300, 9000), (64, 20)], 8, 2)):
+        cache, q, cu, out, lse = check_attn(ksa, rows, Hq, Hkv, 64, 16, True, True, seed=77)
+        ws = torch.zeros(ksa.ksa_chunk_attn_workspace(len(rows), Hq, Hkv, 64,
+                                                      cache.table.shape[1] * 16, q.shape[0]),
+                         dtype=torch.uint8, device=DEV)
+        seq, lse2 = i32([L for _, L in rows]), torch.empty((q.shape[0], Hq), device=DEV)
+        for _ in range(20):
+            got, _ = cache.call(ksa, q, cu, seq, ksa.MASK_CAUSAL, workspace=ws, lse=lse2)
+            assert torch.equal(got, out[:q.shape[0]]) and torch.equal(lse2, lse)
+
+
+def test_serving_calls_on_two_streams_at_once(ksa):
+    """Calls that overlap, each with its own workspace, give what they give alone."""
+    rows = [(3, 30000)]
+    cache, q, cu, out, _ = check_attn(ksa, rows, 8, 2, 128, 16, True, True, seed=55)
+    seq = i32([30000])
+    need = ksa.ksa_chunk_attn_workspace(1, 8, 2, 128, cache.table.shape[1] * 16, 3)
+    lanes = [(torch.cuda.Stream(), torch.zeros(need, dtype=torch.uint8, device=DEV),
+              torch.empty_like(out)) for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for stream, ws, o in lanes:
+            cache.call(ksa, q, cu, seq, ksa.MASK_CAUSAL, out=o, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, o in lanes:
+        assert torch.equal(o, out)
