@@ -799,6 +799,17 @@ def _arg(t, name: str, dtype, shape, dev: int) -> int:
     _reject(t, name, dtype, shape, dev)
 
 
+def _vec(t, name: str, dtype, n: int, dev: int) -> int:
+    """_arg for a vector of n elements."""
+    try:
+        if (t.dtype is dtype and t.numel() == n and t.get_device() == dev and
+                t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _reject(t, name, dtype, (n,), dev)
+
+
 def _extra(t, dev: int):
     """The address of an optional status word."""
     if t is None:
@@ -862,16 +873,16 @@ def ksa_assign_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     ws, ws_ptr, ws_bytes = _scratch(workspace, 256, dev)
     sh = Shape(B, 1, 1, 64, mb * block_size, block_size)
     _run_on(dev, stream, lib().ksa_assign_pages, ctypes.byref(sh),
-            _arg(ctx_lens, "ctx_lens", i32, (B,), dev),
-            _arg(new_lens, "new_lens", i32, (B,), dev),
+            _vec(ctx_lens, "ctx_lens", i32, B, dev),
+            _vec(new_lens, "new_lens", i32, B, dev),
             _arg(block_table, "block_table", i32, (B, mb), dev), mb, pages,
-            _arg(free_pages, "free_pages", i32, (pages,), dev),
-            _arg(num_free, "num_free", i32, (1,), dev),
-            _arg(num_free_out, "num_free_out", i32, (1,), dev), num_tokens,
-            _arg(seq_lens, "seq_lens", i32, (B,), dev),
-            _arg(cu_new, "cu_new", i32, (B + 1,), dev),
-            _arg(slots, "slots", torch.int64, (num_tokens,), dev),
-            _arg(positions, "positions", i32, (num_tokens,), dev), ws_ptr, ws_bytes,
+            _vec(free_pages, "free_pages", i32, pages, dev),
+            _vec(num_free, "num_free", i32, 1, dev),
+            _vec(num_free_out, "num_free_out", i32, 1, dev), num_tokens,
+            _vec(seq_lens, "seq_lens", i32, B, dev),
+            _vec(cu_new, "cu_new", i32, B + 1, dev),
+            _vec(slots, "slots", torch.int64, num_tokens, dev),
+            _vec(positions, "positions", i32, num_tokens, dev), ws_ptr, ws_bytes,
             _extra(dev_status, dev))
     return seq_lens, cu_new, slots, positions
 
@@ -889,10 +900,10 @@ def ksa_release_pages(seq_lens: torch.Tensor, done: torch.Tensor, block_table: t
     ws, ws_ptr, ws_bytes = _scratch(workspace, 256, dev)
     sh = Shape(B, 1, 1, 64, mb * block_size, block_size)
     _run_on(dev, stream, lib().ksa_release_pages, ctypes.byref(sh),
-            _arg(done, "done", i32, (B,), dev), _arg(seq_lens, "seq_lens", i32, (B,), dev),
+            _vec(done, "done", i32, B, dev), _vec(seq_lens, "seq_lens", i32, B, dev),
             _arg(block_table, "block_table", i32, (B, mb), dev), mb, pages,
-            _arg(free_pages, "free_pages", i32, (pages,), dev),
-            _arg(num_free, "num_free", i32, (1,), dev), ws_ptr, ws_bytes,
+            _vec(free_pages, "free_pages", i32, pages, dev),
+            _vec(num_free, "num_free", i32, 1, dev), ws_ptr, ws_bytes,
             _extra(dev_status, dev))
 
 
@@ -984,11 +995,11 @@ def _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged, dev_st
         if slots is None:
             raise ValueError("slots must be given with k and v")
     if slots is not None:
-        slot_ptr = _arg(slots, "slots", torch.int64, (N,), dev)
+        slot_ptr = _vec(slots, "slots", torch.int64, N, dev)
     ref = None
     if rotary is not None:
         ref = rotary._ref
-        pos_ptr = (_arg(positions, "positions", torch.int32, (N,), dev)
+        pos_ptr = (_vec(positions, "positions", torch.int32, N, dev)
                    if rotary.num_axes == 1 and isinstance(positions, torch.Tensor) and
                    positions.dim() == 1
                    else _arg(positions, "positions", torch.int32, (rotary.num_axes, N), dev))
@@ -1060,8 +1071,8 @@ def _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse, wor
     ws, ws_ptr, ws_bytes = _scratch(workspace, need, dev)
     head = (ctypes.byref(sh), N, q.data_ptr(), qs, _arg(K, "K", torch.bfloat16, cache, dev),
             _arg(V, "V", torch.bfloat16, cache, dev))
-    rest = (_arg(cu_q, "cu_q", torch.int32, (B + 1,), dev),
-            _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), mask, scale,
+    rest = (_vec(cu_q, "cu_q", torch.int32, B + 1, dev),
+            _vec(seq_lens, "seq_lens", torch.int32, B, dev), mask, scale,
             _arg(out, "out", torch.bfloat16, (N, Hq, D), dev),
             None if lse is None else _arg(lse, "lse", torch.float32, (N, Hq), dev), ws_ptr,
             ws_bytes, _extra(dev_status, dev))

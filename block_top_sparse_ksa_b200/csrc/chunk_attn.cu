@@ -203,13 +203,13 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
   deepest = __reduce_max_sync(0xffffffffu, deepest);
   if (deepest < 4 || items == 0.f || items > 1e6f) return {0, max(deepest, 1)};
   const int n = static_cast<int>(items), rem = n % ctas;
-  const float mean = tiles / items;
+  const float mean = __fdividef(tiles, items), per_cta = 1.f / ctas;
   const bool equal = mean >= 0.85f * deepest;
   const int cuts = lane < 15 ? lane + 1 : lane == 15 ? max(1, ctas / n) : lane - 14;
   const int s = max(2, ceil_div(deepest, cuts));
   float parts = 0.f, joined = 0.f;  // of cutting all items
   if (a.B <= 32) {
-    const float own = static_cast<float>(first.tiles) * a.Hkv, per = 1.f / s;
+    const float own = static_cast<float>(first.tiles) * a.Hkv, per = __fdividef(1.f, s);
     const int deep = first.deep;
 #pragma unroll 4
     for (int b = 0; b < a.B; ++b) {
@@ -219,21 +219,22 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
       if (c > 1.f) joined += k * c;
     }
   } else {  // all rows as deep as the mean
-    const float c = fmaxf(1.f, ceilf(mean / s));
+    const float c = fmaxf(1.f, ceilf(__fdividef(mean, s)));
     parts = items * c;
     joined = s < deepest ? parts : 0.f;
   }
   float cost;
   if (lane < 16) {
-    cost = equal ? ceilf(parts / ctas) * (tiles / parts + kStart + (joined > 0.f ? kPart : 0.f))
-                 : fmaxf((tiles + kStart * parts + kPart * joined) / ctas + 0.35f * min(s, deepest),
-                         s + kStart);
+    const float each = __fdividef(tiles, parts) + kStart + (joined > 0.f ? kPart : 0.f);
+    const float even = (tiles + kStart * parts + kPart * joined) * per_cta;
+    cost = equal ? ceilf(parts * per_cta) * each
+                 : fmaxf(even + 0.35f * min(s, deepest), s + kStart);
     if (joined > 0.f) cost += join;
   } else {
     joined = static_cast<float>(rem) * cuts;
     cost = equal && rem > 0 && n > ctas
                ? (n / ctas) * (mean + kStart) +
-                     ceilf(joined / ctas) * (mean / cuts + kStart + kPart) + join
+                     ceilf(joined * per_cta) * (__fdividef(mean, cuts) + kStart + kPart) + join
                : INFINITY;
   }
   if (joined > max_parts) cost = INFINITY;

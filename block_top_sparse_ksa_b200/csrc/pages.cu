@@ -8,7 +8,7 @@
 //           = free_pages[F - 1 - (first_b + j - ceil(c_b / bs))]   otherwise.
 // So no CTA waits for another: each scans the rows' lengths itself (they are a
 // few KB out of L2), 1024 rows at a time in shared memory, and expands its own
-// 1024 token places by binary search over the prefix sums.  A new block's first
+// token places by binary search over the prefix sums.  A new block's first
 // token is always a new token, so the thread that has it writes the block's
 // table entry.  Release is the same with the released blocks as the places.
 //
@@ -16,9 +16,10 @@
 // written by the CTA that is the last to have read them (a counter in the
 // workspace, which it sets back to zero).
 //
-// Bound by latency: three dependent loads (lengths, page, then the store), some
-// 4 us at any size that a serving step has; the bytes (12 per token, 8 per new
-// page) are below 2 MB.
+// Bound by latency: three dependent loads (lengths, page, then the store).  256
+// rows of one token take 3.9 us, 64 rows of 139000 tokens 6.1 us; with 500 rows
+// of 625000 tokens the scans in 611 CTAs count, 11.0 us (11.3 with half as many
+// CTAs of twice the places), and the release of their 39000 pages takes 5.6.
 #include "ksa_device.cuh"
 #include "ksa_internal.h"
 
@@ -29,7 +30,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsPerThread = 4;
 constexpr int kChunk = kThreads * kRowsPerThread;  // rows scanned together
-constexpr int kTokens = 1024;                      // token places (or released pages) per CTA
+constexpr int kTokens = 1024;                      // token places per CTA
+constexpr int kPages = 512;                        // released pages per CTA and turn
 
 struct Chunk {           // one chunk of rows, in shared memory
   int place[kChunk + 1];  // first place of each row: cu_b, or pages released before it
@@ -37,6 +39,9 @@ struct Chunk {           // one chunk of rows, in shared memory
   int ctx[kChunk];        // c_b
   int len[kChunk];        // the row's seq_lens after the call
 };
+
+// Blocks of 2^sh tokens that n tokens fill or begin (block sizes are 16, 32 and 64).
+__device__ __forceinline__ int blocks_of(int n, int sh) { return (n + (1 << sh) - 1) >> sh; }
 
 // Exclusive prefix sums over the block of two values per thread, and the totals.
 __device__ __forceinline__ void block_scan2(int &a, int &b, int &ta, int &tb, int2 *scratch) {
@@ -104,7 +109,7 @@ __device__ __forceinline__ bool last_cta(uint32_t *counter, int *flag) {
 __device__ __forceinline__ int scan_assign(const AssignArgs &a, int base, int F, Chunk &c,
                                            int2 *scratch, int &tokens, int &pages,
                                            bool report) {
-  const int rows = min(kChunk, a.B - base);
+  const int rows = min(kChunk, a.B - base), sh = __ffs(a.bs) - 1;
   int n[kRowsPerThread], need[kRowsPerThread], ctx[kRowsPerThread];
   bool bad[kRowsPerThread];
   int sn = 0, sp = 0;
@@ -118,7 +123,7 @@ __device__ __forceinline__ int scan_assign(const AssignArgs &a, int base, int F,
       ctx[i] = min(max(c0, 0), a.T);
       n[i] = min(max(n0, 0), a.T);
       bad[i] = ctx[i] != c0 || n[i] != n0 || n[i] > a.T - ctx[i];
-      if (!bad[i]) need[i] = (ctx[i] + n[i] + a.bs - 1) / a.bs - (ctx[i] + a.bs - 1) / a.bs;
+      if (!bad[i]) need[i] = blocks_of(ctx[i] + n[i], sh) - blocks_of(ctx[i], sh);
     }
     sn += n[i];
   }
@@ -169,6 +174,7 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignArgs
   pdl_wait();
   pdl_launch_dependents();
   const bool reporter = blockIdx.x == 0;
+  const int sh = __ffs(a.bs) - 1;
   const int F0 = *a.num_free, F = min(max(F0, 0), a.num_pages);
   if (reporter && threadIdx.x == 0 && F != F0) flag_status(a.status, KSA_FLAG_NO_PAGE);
   const int t0 = blockIdx.x * kTokens, t1 = min(t0 + kTokens, a.N);
@@ -193,12 +199,12 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignArgs
       if (t >= hi) continue;
       const int r = find_row(c, rows, t);
       if (c.first[r] < 0) continue;
-      const int held = (c.ctx[r] + a.bs - 1) / a.bs;
+      const int held = blocks_of(c.ctx[r], sh);
       pos[i] = c.ctx[r] + (t - c.place[r]);
-      const int j = pos[i] / a.bs;
+      const int j = pos[i] >> sh;
       int *entry = a.block_table + static_cast<size_t>(base + r) * a.max_blocks + j;
       page[i] = j < held ? *entry : a.free_pages[F - 1 - (c.first[r] + j - held)];
-      if (j >= held && pos[i] == j * a.bs) fresh[i] = entry;  // the new block's first token
+      if (j >= held && (pos[i] & (a.bs - 1)) == 0) fresh[i] = entry;  // the new block's first token
     }
 #pragma unroll
     for (int i = 0; i < kTokens / kThreads; ++i) {
@@ -209,7 +215,8 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignArgs
         page[i] = -1;
       }
       if (fresh[i] != nullptr) *fresh[i] = page[i];
-      a.slots[t] = page[i] < 0 ? -1LL : static_cast<long long>(page[i]) * a.bs + pos[i] % a.bs;
+      a.slots[t] =
+          page[i] < 0 ? -1LL : (static_cast<long long>(page[i]) << sh) + (pos[i] & (a.bs - 1));
       a.positions[t] = pos[i];
     }
     if (base + kChunk < a.B) __syncthreads();  // the chunk is read before the next one fills it
@@ -231,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignArgs
     for (int r = threadIdx.x; r < rows; r += kThreads) {
       const int len = c.len[r];
       a.seq_lens[base + r] = len;
-      taken += (len + a.bs - 1) / a.bs - (c.ctx[r] + a.bs - 1) / a.bs;
+      taken += blocks_of(len, sh) - blocks_of(c.ctx[r], sh);
     }
   }
   int zero = 0, total, tz;
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const AssignArgs
 // Scans rows [base, base + kChunk): the blocks each released row gives back.
 __device__ __forceinline__ int scan_release(const ReleaseArgs &a, int base, Chunk &c,
                                             int2 *scratch, int &blocks, bool report) {
-  const int rows = min(kChunk, a.B - base);
+  const int rows = min(kChunk, a.B - base), sh = __ffs(a.bs) - 1;
   int n[kRowsPerThread], sn = 0;
 #pragma unroll
   for (int i = 0; i < kRowsPerThread; ++i) {
@@ -251,7 +258,7 @@ __device__ __forceinline__ int scan_release(const ReleaseArgs &a, int base, Chun
     if (r < rows && a.done[base + r] != 0) {
       const int L = a.seq_lens[base + r], Lc = min(max(L, 0), a.T);
       if (report && L != Lc) flag_status(a.status, KSA_FLAG_SEQ_LEN_CLAMPED);
-      n[i] = (Lc + a.bs - 1) / a.bs;
+      n[i] = blocks_of(Lc, sh);
     }
     sn += n[i];
   }
@@ -296,14 +303,14 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleaseAr
     } else {
       blocks = total;
     }
-    // places are shared out CTA by CTA: e = blockIdx.x * kTokens + ..., then a grid further
-    for (long long e0 = static_cast<long long>(blockIdx.x) * kTokens; e0 < blocks;
-         e0 += static_cast<long long>(gridDim.x) * kTokens) {
-      const int end = static_cast<int>(min(e0 + kTokens, static_cast<long long>(blocks)));
+    // places are shared out CTA by CTA: e = blockIdx.x * kPages + ..., then a grid further
+    for (long long e0 = static_cast<long long>(blockIdx.x) * kPages; e0 < blocks;
+         e0 += static_cast<long long>(gridDim.x) * kPages) {
+      const int end = static_cast<int>(min(e0 + kPages, static_cast<long long>(blocks)));
       const int lo = max(static_cast<int>(e0), before) + threadIdx.x;
-      int *entry[kTokens / kThreads], page[kTokens / kThreads];
+      int *entry[kPages / kThreads], page[kPages / kThreads];
 #pragma unroll
-      for (int i = 0; i < kTokens / kThreads; ++i) {
+      for (int i = 0; i < kPages / kThreads; ++i) {
         const int e = lo + i * kThreads;
         entry[i] = nullptr;
         if (e >= end) continue;
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleaseAr
         page[i] = *entry[i];
       }
 #pragma unroll
-      for (int i = 0; i < kTokens / kThreads; ++i) {
+      for (int i = 0; i < kPages / kThreads; ++i) {
         if (entry[i] == nullptr) continue;
         *entry[i] = -1;
         if (page[i] < 0 || page[i] >= a.num_pages) {
@@ -340,8 +347,8 @@ cudaError_t launch_assign_pages(const AssignArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_release_pages(const ReleaseArgs &a, int num_sms, cudaStream_t stream) {
   const long long most = static_cast<long long>(a.B) * a.max_blocks;  // blocks released at most
-  long long ctas = (most + kTokens - 1) / kTokens;
-  if (ctas > num_sms) ctas = num_sms;
+  long long ctas = (most + kPages - 1) / kPages;
+  if (ctas > 2LL * num_sms) ctas = 2LL * num_sms;
   return launch_pdl(release_pages_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0,
                     stream, a);
 }

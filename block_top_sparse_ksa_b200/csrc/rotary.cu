@@ -27,7 +27,7 @@ constexpr int kThreads = 256;
 // loads each) in flight per thread, three such rounds per CTA and four CTAs per SM (62 registers);
 // 70 with four or eight rounds; 82 with three items and one round (three CTAs per SM: between a
 // CTA's start and its last store lie two memory latencies, which more CTAs cover).
-constexpr int kUnroll = 2, kRounds = 3, kCtas = 4;
+constexpr int kUnroll = 2, kCtas = 4;
 constexpr int kMaxTok = 8;  // tokens per CTA, at most
 
 __device__ __forceinline__ void turn2(uint32_t &a, uint32_t &b, float4 cs) {
@@ -160,16 +160,25 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 }  // namespace
 
 cudaError_t launch_rotary_append(const RotaryArgs &a, int num_sms, cudaStream_t stream) {
-  // as many tokens per CTA as its threads take in kRounds rounds; fewer while that leaves SMs
-  // without work, so that a decode step's tokens spread
+  // tokens per CTA: the least waves x (rounds + 1 for a CTA's start), so that a decode step's
+  // tokens spread over the SMs and a large call ends with full waves (5001 tokens of 48 heads of
+  // 64: 5 tokens in two waves instead of 8 in one and a bit)
   const int heads = (a.q != nullptr ? a.Hq : 0) + (a.k != nullptr ? 2 * a.Hkv : 0);
-  int tok = kRounds * kThreads * kUnroll / (heads * (a.D / 16));
-  const int spread = a.N / (4 * num_sms);
-  if (tok > spread) tok = spread;
-  tok = tok < 1 ? 1 : tok > kMaxTok ? kMaxTok : tok;
+  int tok = 1;
+  long long best = -1;
+  for (int t = 1; t <= (heads <= 4096 ? kMaxTok : 1); ++t) {
+    const long long ctas = (a.N + t - 1) / t, slots = kCtas * num_sms;
+    const long long waves = (ctas + slots - 1) / slots;
+    const long long per = static_cast<long long>(t) * heads * (a.D / 16);
+    const long long cost = waves * ((per + kThreads * kUnroll - 1) / (kThreads * kUnroll) + 1);
+    if (best < 0 || cost < best) {
+      best = cost;
+      tok = t;
+    }
+  }
   const dim3 grid(static_cast<unsigned>((a.N + tok - 1) / tok)), block(kThreads);
-  // x / heads = umulhi(x, per_head) for the x < tok * heads of more than one token, since then
-  // heads <= 384: the product's error, below x * heads / 2^32, stays below 1 / heads
+  // x / heads = umulhi(x, per_head) for x < tok * heads: the quotient's error, below x / 2^32,
+  // stays below 1 / heads, since tok * heads^2 < 2^32
   const uint32_t per_head = static_cast<uint32_t>((0x100000000ull + heads - 1) / heads);
   if (a.D == 128)
     return launch_pdl(rotary_append_kernel<128>, grid, block, 0, stream, a, tok, per_head);
