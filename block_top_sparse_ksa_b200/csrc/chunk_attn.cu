@@ -14,11 +14,16 @@
 // Layout.  One CTA per SM holds two streams, each with its S (whose first half
 // P overwrites) and O in tensor memory (2 x (128 + D) of 512 columns) and four
 // softmax warps of one row per thread: no shuffles.  While one stream's softmax
-// runs, the tensor cores work for the other.  PAIR: the streams are two query
-// tiles over the same key tiles.  Otherwise (few query rows per sequence) they
-// are one query tile over the even and the odd key tiles, joined at the end.
-// One warp loads (TMA; a page's rows of one kv-head are one box), one issues
-// the products, one hands out the work.  Keys and values share one ring.
+// runs, the tensor cores work for the other.
+//   kPair  the streams are two query tiles over the same key tiles.
+//   kOne   one query tile over the even and the odd key tiles, joined at the end.
+//   kFew   as kOne with 32 query rows, four times in the tile: warp w of a stream
+//          weighs only the keys [32 w, 32 w + 32) of a key tile (the other
+//          weights of its copy are 0), so the four copies' outputs add up to the
+//          rows' and the softmax of a tile takes a fourth of the time.  With few
+//          rows the call is bound by reading K and V, and only then.
+// Two warps load keys and values (TMA; a page's rows of one kv-head are one
+// box), one issues the products, one hands out the work.
 //
 // Work.  Items are (row, kv-head, tokens of a CTA), longest first within a row;
 // the CTAs stay and take the next item when they are done, so that an item's
@@ -37,7 +42,7 @@ namespace {
 constexpr int kQ = 128;        // query rows of a tile
 constexpr int kKeys = 128;     // key tokens of a tile
 constexpr int kSoftWarps = 8;  // four per stream
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kWorkWarp = 10;
+constexpr int kMmaWarp = 8, kKeyWarp = 9, kWorkWarp = 10, kValueWarp = 11;
 // A thread is launched with 65536 / 384 registers, 168.  The softmax keeps a row of 128 scores
 // in registers, so the third warpgroup passes its share on: 2 x 224 + 56 = 3 x 168.
 constexpr int kThreads = 384;
@@ -50,14 +55,20 @@ constexpr int kLead = 4, kLag = 10;  // stagger of the weights' loop, in pairs o
 constexpr float kRescale = 8.f;      // log2 of the largest weight before m moves
 constexpr int kCtlBytes = 3072;
 
-template <int D, bool PAIR>
+enum Mode { kPair, kOne, kFew };
+
+template <int D, Mode MODE>
 struct Cfg {
+  static constexpr bool kPairs = MODE == kPair, kFews = MODE == kFew;
   static constexpr int kQBytes = kQ * D * 2, kTileBytes = kKeys * D * 2;  // of Q, of K or V
-  static constexpr int kQTiles = PAIR ? 2 : 1;
-  static constexpr int kStages = (224 * 1024 - kQTiles * kQBytes) / kTileBytes;
-  static constexpr int kRows = kQ * kQTiles;      // query rows of a CTA
-  static constexpr int kAhead = PAIR ? 1 : 2;     // key tiles whose scores are in use
-  static constexpr int kSmem = kQTiles * kQBytes + kStages * kTileBytes + kCtlBytes;
+  static constexpr int kQTiles = kPairs ? 2 : 1;
+  static constexpr int kSumBytes = kFews ? 2 * D * 32 * 4 : 0;  // of the copies' sum, [2][D][32]
+  // places of the rings: as many tiles as fit, the odd one for values (a tile's keys are done
+  // with one product, its values wait for the softmax)
+  static constexpr int kFit = (224 * 1024 - kQTiles * kQBytes - kSumBytes) / kTileBytes;
+  static constexpr int kKeyPlaces = kFit / 2, kValuePlaces = kFit - kKeyPlaces;
+  static constexpr int kRows = kFews ? 32 : kQ * kQTiles;  // query rows of a CTA
+  static constexpr int kSmem = kQTiles * kQBytes + kFit * kTileBytes + kSumBytes + kCtlBytes;
 };
 
 struct Work {
@@ -70,7 +81,7 @@ struct Work {
 };
 
 struct Ctl {  // in shared memory
-  uint64_t q_full, q_empty, full[16], empty[16];
+  uint64_t q_full, q_empty, k_full[8], k_empty[8], v_full[8], v_empty[8];
   // per stream: scores ready, first half of the weights and all of them ready, product with V done
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
   uint64_t work_full[kWork], work_empty[kWork], soft, drain;
@@ -376,17 +387,17 @@ struct Take {
 
 // The join of an item's parts, by the softmax warps.  First each row's (m, 1 / l) over the parts,
 // in their order, and its lse.
-template <int D, bool PAIR>
+template <int D, Mode MODE>
 __device__ __noinline__ void join_stats(const Params &p, const Work &w, float2 *stats, int TQ,
                                         int G, float c) {
   const ChunkArgs &a = p.a;
-  constexpr int kRows = Cfg<D, PAIR>::kRows;
+  constexpr int kRows = Cfg<D, MODE>::kRows;
   constexpr size_t pitch = kRows * (D + 2);
   const float *base = p.part + static_cast<size_t>(w.slot) * pitch;
   const int rows = w.tokens * G, parts = w.parts;
   for (int rr = threadIdx.x; rr < rows; rr += kSoftWarps * 32) {
     const int tok = rr / G, hh = rr % G;
-    const int row = (PAIR ? (tok / TQ) * kQ + (tok % TQ) * G : tok * G) + hh;
+    const int row = (MODE == kPair ? (tok / TQ) * kQ + (tok % TQ) * G : tok * G) + hh;
     float m = -INFINITY, l = 0.f;
     for (int q0 = 0; q0 < parts; q0 += 16) {  // 16 parts in flight
       float2 ml[16];
@@ -415,11 +426,11 @@ __device__ __noinline__ void join_stats(const Params &p, const Work &w, float2 *
 
 // ... and the outputs, after the warps have met.  A thread adds up 4 dims of a row at a time, parts
 // in order, 4 parts of 4 such quads in flight: the parts come out of L2, some 700 cycles away.
-template <int D, bool PAIR>
+template <int D, Mode MODE>
 __device__ __noinline__ void join_outputs(const Params &p, const Work &w, const float2 *stats,
                                           int TQ, int G, float c) {
   const ChunkArgs &a = p.a;
-  constexpr int kRows = Cfg<D, PAIR>::kRows, kThr = kSoftWarps * 32, kQuads = 4;
+  constexpr int kRows = Cfg<D, MODE>::kRows, kThr = kSoftWarps * 32, kQuads = 4;
   constexpr size_t pitch = kRows * (D + 2);
   const float *base = p.part + static_cast<size_t>(w.slot) * pitch;
   const int rows = w.tokens * G, work = rows * (D / 4), parts = w.parts;
@@ -431,7 +442,7 @@ __device__ __noinline__ void join_outputs(const Params &p, const Work &w, const 
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
       const int e = min(e0 + i * kThr, work - 1), rr = e % rows, tok = rr / G, hh = rr % G;
-      const int row = (PAIR ? (tok / TQ) * kQ + (tok % TQ) * G : tok * G) + hh;
+      const int row = (MODE == kPair ? (tok / TQ) * kQ + (tok % TQ) * G : tok * G) + hh;
       src[i] = base + 2 * row;
       quad[i] = 2 * kRows + (e / rows) * 4 * kRows + 4 * row - 2 * row;
       st[i] = stats[rr];
@@ -476,18 +487,21 @@ __device__ __noinline__ void join_outputs(const Params &p, const Work &w, const 
 
 // ---------------------------------------------------------------------------
 
-template <int D, bool PAIR>
+template <int D, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                       const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ Params p) {
-  using C = Cfg<D, PAIR>;
-  constexpr int NST = C::kStages, A = C::kAhead;
+  using C = Cfg<D, MODE>;
+  constexpr bool PAIR = C::kPairs, FEW = C::kFews;
+  constexpr int NK = C::kKeyPlaces, NV = C::kValuePlaces;
+  constexpr int A = PAIR ? 1 : 2;  // key tiles whose scores are in use
   extern __shared__ __align__(1024) uint8_t tiles[];
-  uint8_t *ring = tiles + C::kQTiles * C::kQBytes;
-  Ctl &ctl = *reinterpret_cast<Ctl *>(ring + NST * C::kTileBytes);
-  static_assert(sizeof(Ctl) <= kCtlBytes && NST <= 16, "");
+  uint8_t *k_ring = tiles + C::kQTiles * C::kQBytes, *v_ring = k_ring + NK * C::kTileBytes;
+  float *sums = reinterpret_cast<float *>(v_ring + NV * C::kTileBytes);
+  Ctl &ctl = *reinterpret_cast<Ctl *>(v_ring + NV * C::kTileBytes + C::kSumBytes);
+  static_assert(sizeof(Ctl) <= kCtlBytes && NK >= 2 && NV <= 8 && NK < kBadRing, "");
   static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168 && C::kSmem <= 227 * 1024, "");
   const ChunkArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -497,9 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       mbar_init(&ctl.q_full, 1);
       mbar_init(&ctl.q_empty, 1);
-      for (int i = 0; i < NST; ++i) {
-        mbar_init(&ctl.full[i], 1);
-        mbar_init(&ctl.empty[i], 1);
+      for (int i = 0; i < 8; ++i) {
+        mbar_init(&ctl.k_full[i], 1);
+        mbar_init(&ctl.k_empty[i], 1);
+        mbar_init(&ctl.v_full[i], 1);
+        mbar_init(&ctl.v_empty[i], 1);
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&ctl.s_full[s], 1);
@@ -509,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int i = 0; i < kWork; ++i) {
         mbar_init(&ctl.work_full[i], 1);
-        mbar_init(&ctl.work_empty[i], kSoftWarps + 2);
+        mbar_init(&ctl.work_empty[i], kSoftWarps + 3);
       }
       mbar_init(&ctl.soft, kSoftWarps);
       mbar_init(&ctl.drain, 1);
@@ -519,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tmem_alloc(&ctl.tmem, 512);
     tmem_fence_before();
-  } else if (warp == kLoadWarp && lane == 0) {
+  } else if (warp == kKeyWarp && lane == 0) {
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
@@ -534,33 +550,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWorkWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     hand_out_work(p, ctl, TT, rows);
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kKeyWarp || warp == kValueWarp) {
     // ------------------------------------------------------------ loads
+    // Two warps, for a page of 16 tokens takes a copy each, and a warp issues one in some 60
+    // cycles: with one warp, cross attention of one token over pages of 16 (32 sequences, 16 heads
+    // of 64, 200 to 1500 states) took 46.6 us instead of 36.5.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    const bool paged = a.kv.table != nullptr;
+    const bool keys = warp == kKeyWarp, paged = a.kv.table != nullptr;
     const int bs = paged ? a.kv.bs : kKeys, ppt = kKeys / bs;  // boxes of a tile and half
     const int groups = 32 / ppt;                               // tiles whose ids 32 lanes hold
     const int box = lane % ppt, half = lane / ppt;
     const int none = static_cast<int>(  // a row past the pool: the box reads as zeros
         paged ? static_cast<long long>(a.kv.num_pages) * a.Hkv * bs
               : static_cast<long long>(a.B) * a.Hkv * a.T);
+    const CUtensorMap *map = keys ? &k_map : &v_map;
+    uint8_t *ring = keys ? k_ring : v_ring;
+    uint64_t *full = keys ? ctl.k_full : ctl.v_full, *empty = keys ? ctl.k_empty : ctl.v_empty;
+    const int places = keys ? NK : NV;
     int stage = 0, puts = 0, mark = 0;
     uint32_t drained = 1, q_turn = 1;  // a place's first filling waits for nothing
     bool ok = true;
-    auto put = [&](const CUtensorMap *map, int y) {  // one tile into the next place
-      ok = wait_bar(&ctl.empty[stage], drained, &ctl.abort);
+    auto load_q = [&](const Work &w) {
+      ok = wait_bar(&ctl.q_empty, q_turn, &ctl.abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[stage], C::kTileBytes);
-      __syncwarp();
-      if (lane < ppt * (D / 64))
-        tma_load_2d(ring + stage * C::kTileBytes + half * (kKeys * 128) + box * bs * 128, map,
-                    half * 64, y, &ctl.full[stage]);
-      ++puts;
-      if (++stage == NST) {
-        stage = 0;
-        drained ^= 1u;
+      q_turn ^= 1u;
+      if (lane == 0) {
+        const int boxes = FEW ? 4 : PAIR && w.tokens > TQ ? 2 : 1;  // copies, or tiles
+        mbar_arrive_expect_tx(&ctl.q_full, static_cast<uint32_t>(boxes * G * TQ * D * 2));
+        for (int i = 0; i < boxes; ++i)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(tiles + i * (FEW ? 32 * 128 : C::kQBytes) + h * (kQ * 128), &q_map, h * 64,
+                        w.g * G, w.token + (FEW ? 0 : i * TQ), &ctl.q_full);
       }
+      __syncwarp();
     };
     Take take;
     Work w;
@@ -573,75 +596,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = (w.t0 + group * groups) * ppt + lane;
         return paged && j < blocks && j < a.kv.max_blocks ? __ldg(table + j) : -1;
       };
-      int ids = load_ids(0), next = load_ids(1), group = 0;
-      int y_ring[A];  // K runs A tiles ahead of V; the rows of the tiles between
-      for (int j = 0; j < w.nt + A && ok; ++j) {
-        if (j == A) {  // the first keys are on their way: now the queries
-          ok = wait_bar(&ctl.q_empty, q_turn, &ctl.abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          q_turn ^= 1u;
-          const int q_tiles = PAIR && w.tokens > TQ ? 2 : 1;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&ctl.q_full, static_cast<uint32_t>(q_tiles * G * TQ * D * 2));
-            for (int s = 0; s < q_tiles; ++s)
-              for (int h = 0; h < D / 64; ++h)
-                tma_load_3d(tiles + s * C::kQBytes + h * (kQ * 128), &q_map, h * 64, w.g * G,
-                            w.token + s * TQ, &ctl.q_full);
-          }
-          __syncwarp();
-        }
-        if (j >= A) put(&v_map, y_ring[0]);  // of tile j - A
-#pragma unroll
-        for (int i = 0; i + 1 < A; ++i) y_ring[i] = y_ring[i + 1];
-        if (j >= w.nt || !ok) continue;
+      int ids = load_ids(0), next = load_ids(1), in_group = 0, group = 0;
+      for (int j = 0; j < w.nt && ok; ++j) {
         int y = none;
         uint32_t bad = 0u;
         if (paged) {
-          if (j / groups != group) {
+          if (in_group == groups) {
             ids = next;
             next = load_ids(++group + 1);
+            in_group = 0;
           }
           const int block = (w.t0 + j) * ppt + box;
-          const int id = __shfl_sync(0xffffffffu, ids, (j % groups) * ppt + box);
+          const int id = __shfl_sync(0xffffffffu, ids, in_group++ * ppt + box);
           const bool inside = block < blocks, good = id >= 0 && id < a.kv.num_pages;
           if (inside && good) y = (id * a.Hkv + w.g) * bs;
           bad = __ballot_sync(0xffffffffu, lane < ppt && inside && !good);
         } else {
           y = (w.b * a.Hkv + w.g) * a.T + (w.t0 + j) * kKeys;
         }
-        if (lane == 0) {
+        if (keys && lane == 0) {
           ctl.bad[mark] = bad;
           if (bad != 0u) flag_status(a.status, KSA_FLAG_INDEX_SKIPPED);
         }
         mark = (mark + 1) % kBadRing;
-        put(&k_map, y);
-        y_ring[A - 1] = y;
+        ok = wait_bar(&empty[stage], drained, &ctl.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::kTileBytes);
+        __syncwarp();
+        if (lane < ppt * (D / 64))
+          tma_load_2d(ring + stage * C::kTileBytes + half * (kKeys * 128) + box * bs * 128, map,
+                      half * 64, y, &full[stage]);
+        ++puts;
+        if (++stage == places) {
+          stage = 0;
+          drained ^= 1u;
+        }
+        if (keys && j == 0) load_q(w);  // the first keys are on their way: now the queries
       }
       take.release(ctl);
     }
     // leave no copy in flight behind (also after an aborted wait)
-    for (int i = max(0, puts - NST); i < puts; ++i) mbar_wait(&ctl.full[i % NST], (i / NST) & 1);
-    mbar_wait(&ctl.q_full, q_turn);
+    for (int i = max(0, puts - places); i < puts; ++i)
+      mbar_wait(&full[i % places], (i / places) & 1);
+    if (keys) mbar_wait(&ctl.q_full, q_turn);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     constexpr uint32_t idesc_s = mma_idesc_bf16(kQ, kKeys, false);
     constexpr uint32_t idesc_o = mma_idesc_bf16(kQ, D, true);
     const uint64_t q_desc = smem_desc_128b(smem_addr(tiles), 16, 1024);
-    const uint64_t k_desc = smem_desc_128b(smem_addr(ring), 16, 1024);
-    const uint64_t v_desc = smem_desc_128b(smem_addr(ring), kKeys * 128, 1024);
+    const uint64_t k_desc = smem_desc_128b(smem_addr(k_ring), 16, 1024);
+    const uint64_t v_desc = smem_desc_128b(smem_addr(v_ring), kKeys * 128, 1024);
     const uint32_t one = elect_one();
-    int stage = 0;                     // next place of the ring, and the parity of its filling
-    uint32_t fill = 0, q_turn = 0;
-    uint32_t p_turn[2] = {0, 0};       // parity of each stream's next weights
+    int k_next = 0, v_next = 0;  // next places of the rings, and the parities of their filling
+    uint32_t k_turn = 0, v_turn = 0, q_turn = 0;
+    uint32_t p_turn[2] = {0, 0};  // parity of each stream's next weights
     bool ok = true;
-    auto next_place = [&]() {  // waits for it
-      const int st = stage;
-      ok = ok && wait_bar(&ctl.full[st], fill, &ctl.abort);
-      if (++stage == NST) {
-        stage = 0;
-        fill ^= 1u;
+    auto next_keys = [&]() {  // waits for the next key tile: its place
+      const int st = k_next;
+      ok = ok && wait_bar(&ctl.k_full[st], k_turn, &ctl.abort);
+      if (++k_next == NK) {
+        k_next = 0;
+        k_turn ^= 1u;
       }
       return st;
     };
@@ -662,10 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                  kd + static_cast<uint64_t>(((i / 4) * (kKeys * 128) + (i % 4) * 32) >> 4), idesc_s,
                  i > 0);
         mma_commit(one, &ctl.s_full[s]);
-        if (!PAIR || s == streams - 1) mma_commit(one, &ctl.empty[st]);
+        if (!PAIR || s == streams - 1) mma_commit(one, &ctl.k_empty[st]);
       };
       for (int j = 0; j < min(A, w.nt); ++j) {
-        const int st = next_place();
+        const int st = next_keys();
         if (j == 0) {
           ok = ok && wait_bar(&ctl.q_full, q_turn, &ctl.abort);
           q_turn ^= 1u;
@@ -679,16 +696,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (w.nt <= A) mma_commit(one, &ctl.q_empty);
       for (int j = 0; j < w.nt && ok; ++j) {
-        const int sv = next_place();
+        const int sv = v_next;
         int sk = 0;
+        ok = wait_bar(&ctl.v_full[sv], v_turn, &ctl.abort);
         if (!ok) break;
+        if (++v_next == NV) {
+          v_next = 0;
+          v_turn ^= 1u;
+        }
         if ((w.t0 + j + 1) * kKeys > w.len) {
           // the cache behind the row's last token: P is 0 there, but 0 x NaN is not
           const int r0 = w.len - (w.t0 + j) * kKeys;
           for (int e = r0 * 8 + lane; e < kKeys * 8; e += 32)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
-              *reinterpret_cast<uint4 *>(ring + sv * C::kTileBytes + h * (kKeys * 128) + e * 16) =
+              *reinterpret_cast<uint4 *>(v_ring + sv * C::kTileBytes + h * (kKeys * 128) + e * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           __syncwarp();
@@ -715,9 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             p_turn[1] ^= 1u;
           mma_commit(one, &ctl.o_done[s]);
-          if (!PAIR || s == streams - 1) mma_commit(one, &ctl.empty[sv]);
+          if (!PAIR || s == streams - 1) mma_commit(one, &ctl.v_empty[sv]);
           if (j + A < w.nt) {
-            if (i == 0) sk = next_place();
+            if (i == 0) sk = next_keys();
             if (!ok) break;
             tmem_fence_after();
             scores(s, sk);
@@ -734,7 +756,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kSoftWarps) {
     // ------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int s = warp >> 2, r = (warp & 3) * 32 + lane;  // stream, row of the query tile
+    // stream, row of the query tile (of the statistics: every copy's), row of the queries
+    const int s = warp >> 2, r = (warp & 3) * 32 + lane, qr = FEW ? lane : r;
+    constexpr int kCols = FEW ? 32 : kKeys;  // keys that a thread weighs, from col0 on
+    const int col0 = FEW ? (warp & 3) * 32 : 0;
     const float c = a.scale * kLog2e;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kKeys, to = tmem + lanes + 2 * kKeys + s * D;
@@ -756,8 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Work w;
         ok = take.get(ctl, w);
         if (!ok || w.token < 0) break;
-        const int tok = r / G + (PAIR ? s * TQ : 0);
-        const bool valid = r < G * TQ && tok < w.tokens;
+        const int tok = qr / G + (PAIR ? s * TQ : 0);
+        const bool valid = qr < G * TQ && tok < w.tokens;
         active = __any_sync(0xffffffffu, valid);
         steps = PAIR ? (s == 0 || w.tokens > TQ ? w.nt : 0) : (w.nt - s + 1) / 2;
         end = (valid ? (a.causal ? w.seen + tok : w.len) : 0) - w.t0 * kKeys;
@@ -771,27 +796,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         turn ^= 1u;
         tmem_fence_after();
         if (active) {
-          uint32_t v[kKeys];
+          uint32_t v[kCols];
+          if constexpr (FEW) {
+            tmem_load32(ts + col0, v);
+          } else {
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 64) tmem_load64(ts + i, v + i);
-          const int lim = end - j * kKeys;
+            for (int i = 0; i < kCols; i += 64) tmem_load64(ts + i, v + i);
+          }
+          const int lim = end - j * kKeys - col0;
           const uint32_t bad = ctl.bad[(mark + j) % kBadRing];
-          if (lim < kKeys) {
+          if (lim < kCols) {
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i)
+            for (int i = 0; i < kCols; ++i)
               if (i >= lim) v[i] = 0xff800000u;
           }
           if (bad != 0u) {
             const int sh = __ffs(a.kv.bs) - 1;
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i)
-              if ((bad >> (i >> sh)) & 1u) v[i] = 0xff800000u;
+            for (int i = 0; i < kCols; ++i)
+              if ((bad >> ((col0 + i) >> sh)) & 1u) v[i] = 0xff800000u;
           }
           float mx[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < kKeys; i += 2)
+          for (int i = 0; i < kCols; i += 2)
             mx[(i >> 1) & 7] = max3_nan(mx[(i >> 1) & 7], __uint_as_float(v[i]),
                                         __uint_as_float(v[i + 1]));
           const float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]),
@@ -818,18 +847,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t cc = f32x2(c, c), mm = f32x2(-ms, -ms);
           uint64_t sum[2] = {0, 0};
           uint32_t x[16];
+          if (FEW) {  // the copy's other weights
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = 0u;
+#pragma unroll
+            for (int i = 16; i < kKeys / 2; i += 16) tmem_store16(ts + (col0 / 2 + i) % (kKeys / 2), x);
+          }
           // a pair's scale, exponential, and sum and rounding run staggered, so that the
           // exponential unit (8 cycles a warp instruction) does not wait for them
 #pragma unroll
-          for (int e = 0; e < kKeys / 2 + kLag; ++e) {
-            if (e < kKeys / 2) {
+          for (int e = 0; e < kCols / 2 + kLag; ++e) {
+            if (e < kCols / 2) {
               float x0, x1;
               f32x2_split(fma2(f32x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
                                cc, mm), x0, x1);
               v[2 * e] = __float_as_uint(x0);
               v[2 * e + 1] = __float_as_uint(x1);
             }
-            if (e >= kLead && e - kLead < kKeys / 2) {
+            if (e >= kLead && e - kLead < kCols / 2) {
               exp2_in_place(v[2 * (e - kLead)]);
               exp2_in_place(v[2 * (e - kLead) + 1]);
             }
@@ -838,8 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float p0 = __uint_as_float(v[2 * d]), p1 = __uint_as_float(v[2 * d + 1]);
               sum[d & 1] = add2(sum[d & 1], f32x2(p0, p1));
               x[d & 15] = pack_bf16x2(p0, p1);
-              if ((d & 15) == 15) tmem_store16(ts + (d & ~15), x);
-              if (d == kKeys / 4 - 1) {  // the first half of the weights: their products may start
+              if ((d & 15) == 15) tmem_store16(ts + col0 / 2 + (d & ~15), x);
+              if (!FEW && d == kKeys / 4 - 1) {  // the first half of the weights: their products may start
                 tmem_wait_st();
                 tmem_fence_before();
                 __syncwarp();
@@ -851,19 +886,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           f32x2_split(add2(sum[0], sum[1]), l0, l1);
           l += l0 + l1;
           tmem_wait_st();
-        } else if (lane == 0) {
-          mbar_arrive(&ctl.p_half[s]);
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full[s]);
+        if (lane == 0) {
+          if (FEW || !active) mbar_arrive(&ctl.p_half[s]);
+          mbar_arrive(&ctl.p_full[s]);
+        }
       }
       if (!ok) break;
       // -------------------------------------------------------- output
       const Work &w = ctl.work[take.at];
       mark = (mark + w.nt) % kBadRing;
-      const int tok = r / G + (PAIR ? s * TQ : 0), h = w.g * G + r % G;
-      const bool valid = r < G * TQ && tok < w.tokens;
+      const int tok = qr / G + (PAIR ? s * TQ : 0), h = w.g * G + qr % G;
+      const bool valid = qr < G * TQ && tok < w.tokens;
       const long long at = (static_cast<long long>(w.token) + tok) * a.Hq + h;
       float f0 = 1.f, f1 = 0.f;
       bool has0 = steps > 0, has1 = false;
@@ -874,6 +910,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_fence_before();
         soft_sync();
         if (!ok) break;
+      }
+      if (FEW) {  // the row's eight maxima and sums
+        const float own = m;
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, ctl.ml[i >> 2][(i & 3) * 32 + lane].x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 y = ctl.ml[i >> 2][(i & 3) * 32 + lane];
+          l += y.x == -INFINITY ? y.y : y.y * fast_exp2((y.x - m) * c);
+        }
+        f0 = own == -INFINITY ? 0.f : fast_exp2((own - m) * c);
+      } else if (!PAIR) {
         const float2 y = ctl.ml[s ^ 1][r];
         has1 = w.nt > (s ^ 1);
         const float both = fmaxf(m, y.x);
@@ -886,33 +936,73 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tmem_fence_after();
       const bool split = w.parts > 1;
-      constexpr int kCols = PAIR ? D : D / 2;  // of this warp
-      const int col0 = PAIR ? 0 : s * kCols;
+      constexpr int kDims = PAIR ? D : D / 2;  // of this warp
+      const int dim0 = PAIR ? 0 : s * kDims;
       float *part = p.part + static_cast<size_t>(w.slot + w.z) * (C::kRows * (D + 2));
-      const int row = (PAIR ? s * kQ : 0) + r;
+      const int row = (PAIR ? s * kQ : 0) + qr;
       const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;
       f0 *= inv;
       f1 *= inv;
-      if (valid && col0 == 0) {
+      if (valid && (FEW ? warp == 0 : dim0 == 0)) {
         if (split)
           reinterpret_cast<float2 *>(part)[row] = make_float2(m, l);
         else if (a.lse != nullptr)
           a.lse[at] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
       }
-      if (active) {
+      if (FEW) {
+        // the copies and streams add up in shared memory: two sums (of the streams), in four
+        // rounds, in each of which the warps of a stream are at different dims
+        constexpr int kBlock = D / 4;
+        for (int i = 0; i < 4; ++i) {
+          const int block = ((warp + i) & 3) * kBlock;
+          float *sum = sums + s * (D * 32) + block * 32 + lane;
 #pragma unroll
-        for (int i = 0; i < kCols; i += 32) {
+          for (int d = 0; d < kBlock; d += 16) {
+            uint32_t v[16];
+            if (has0) tmem_load16(to + block + d, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = has0 ? __uint_as_float(v[e]) * f0 : 0.f;
+              sum[(d + e) * 32] = i == 0 ? x : sum[(d + e) * 32] + x;
+            }
+          }
+          soft_sync();
+        }
+        if (!ok) break;
+        constexpr int kOut = D / 8;  // dims that a thread writes
+        const float *sum = sums + warp * kOut * 32 + lane;
+        float o[kOut];
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) o[e] = sum[e * 32] + sum[D * 32 + e * 32];
+        if (valid && split) {
+          float4 *dst =
+              reinterpret_cast<float4 *>(part + 2 * C::kRows) + warp * kOut / 4 * C::kRows + row;
+#pragma unroll
+          for (int e = 0; e < kOut / 4; ++e)
+            dst[e * C::kRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else if (valid) {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + warp * kOut);
+#pragma unroll
+          for (int e = 0; e < kOut / 8; ++e)
+            dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
+                                pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
+                                pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+        }
+      } else if (active) {
+#pragma unroll
+        for (int i = 0; i < kDims; i += 32) {
           uint32_t v[32];
           float o[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
           if (has0) {
-            tmem_load32(to + col0 + i, v);
+            tmem_load32(to + dim0 + i, v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * f0;
           }
           if (has1) {
-            tmem_load32(tmem + lanes + 2 * kKeys + (s ^ 1) * D + col0 + i, v);
+            tmem_load32(tmem + lanes + 2 * kKeys + (s ^ 1) * D + dim0 + i, v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(v[e]) * f1;
           }
@@ -920,12 +1010,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (split) {
             // [dims / 4][rows][4]: a warp's rows are neighbours
             float4 *dst = reinterpret_cast<float4 *>(part + 2 * C::kRows) +
-                          (col0 + i) / 4 * C::kRows + row;
+                          (dim0 + i) / 4 * C::kRows + row;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               dst[e * C::kRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           } else {
-            uint16_t *dst = a.out + at * D + col0 + i;
+            uint16_t *dst = a.out + at * D + dim0 + i;
             uint32_t x[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
@@ -954,10 +1044,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (ctl.last) {
           __threadfence();
-          join_stats<D, PAIR>(p, w, &ctl.ml[0][0], TQ, G, c);
+          join_stats<D, MODE>(p, w, &ctl.ml[0][0], TQ, G, c);
           soft_sync();
           if (!ok) break;
-          join_outputs<D, PAIR>(p, w, &ctl.ml[0][0], TQ, G, c);
+          join_outputs<D, MODE>(p, w, &ctl.ml[0][0], TQ, G, c);
           soft_sync();  // before the statistics' place is used again
           if (!ok) break;
         }
@@ -966,8 +1056,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       take.release(ctl);
     }
     tmem_fence_before();
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
 
   __syncthreads();
@@ -985,20 +1073,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Two query tiles per CTA where the rows of an average sequence fill more than one.
-bool use_pairs(int B, int Hq, int Hkv, int N) {
-  return static_cast<long long>(N) * (Hq / Hkv) > static_cast<long long>(kQ) * B;
+// By the rows (tokens times heads of a group) of an average sequence: what fills more than a tile
+// of 128 goes in pairs (both tiles then share their keys' loads), what fits in 32 as kFew.  One
+// token over 200 to 1500 states (32 sequences, 16 heads of 64): 36.5 us as kFew, 45.0 as kOne;
+// 5 tokens over 131000 (32 heads on 8 of 128): 96.6 and 100.3.
+Mode choose_mode(int B, int Hq, int Hkv, int N) {
+  const int G = Hq / Hkv;
+  const long long rows = static_cast<long long>(N) * G;
+  return rows > static_cast<long long>(kQ) * B           ? kPair
+         : G <= 32 && rows <= static_cast<long long>(32) * B ? kFew
+                                                           : kOne;
 }
 
-template <int D, bool PAIR>
+int rows_of(Mode mode) { return mode == kPair ? 2 * kQ : mode == kOne ? kQ : 32; }
+
+template <int D, Mode MODE>
 cudaError_t launch(const Params &p, const CUtensorMap *maps, int num_sms, cudaStream_t stream) {
   int occ = 0;
-  auto kernel = chunk_attn_kernel<D, PAIR>;
+  auto kernel = chunk_attn_kernel<D, MODE>;
   const cudaError_t err = kernel_occupancy(reinterpret_cast<const void *>(kernel), kThreads,
-                                           Cfg<D, PAIR>::kSmem, &occ);
+                                           Cfg<D, MODE>::kSmem, &occ);
   if (err != cudaSuccess) return err;
-  kernel<<<num_sms, kThreads, Cfg<D, PAIR>::kSmem, stream>>>(maps[0], maps[1], maps[2], p);
+  kernel<<<num_sms, kThreads, Cfg<D, MODE>::kSmem, stream>>>(maps[0], maps[1], maps[2], p);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_mode(Mode mode, const Params &p, const CUtensorMap *maps, int num_sms,
+                        cudaStream_t stream) {
+  return mode == kPair  ? launch<D, kPair>(p, maps, num_sms, stream)
+         : mode == kOne ? launch<D, kOne>(p, maps, num_sms, stream)
+                        : launch<D, kFew>(p, maps, num_sms, stream);
 }
 
 size_t sem_bytes(int max_parts) {
@@ -1011,7 +1116,7 @@ size_t sem_bytes(int max_parts) {
 // between calls), then the parts
 size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int N, int num_sms) {
   const int max_parts = kPartsPerSm * num_sms;
-  const size_t rows = (use_pairs(B, Hq, Hkv, N) ? 2 : 1) * kQ;
+  const size_t rows = rows_of(choose_mode(B, Hq, Hkv, N));
   return sem_bytes(max_parts) + static_cast<size_t>(max_parts) * rows * (D + 2) * 4;
 }
 
@@ -1023,7 +1128,8 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStr
   p.done = p.next + 1;
   p.sem = p.next + 64;
   p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + sem_bytes(p.max_parts));
-  p.tq = kQ / (a.Hq / a.Hkv);
+  const Mode mode = choose_mode(a.B, a.Hq, a.Hkv, a.N);
+  p.tq = (mode == kFew ? 32 : kQ) / (a.Hq / a.Hkv);
   p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   const bool paged = a.kv.table != nullptr;
   const uint64_t rows = paged ? static_cast<uint64_t>(a.kv.num_pages) * a.Hkv * a.kv.bs
@@ -1034,12 +1140,8 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStr
       !encode_kv_tensor_map(&maps[1], a.K, rows, a.D, box) ||
       !encode_kv_tensor_map(&maps[2], a.V, rows, a.D, box))
     return cudaErrorInvalidValue;
-  const bool pair = use_pairs(a.B, a.Hq, a.Hkv, a.N);
-  if (a.D == 128)
-    return pair ? launch<128, true>(p, maps, num_sms, stream)
-                : launch<128, false>(p, maps, num_sms, stream);
-  return pair ? launch<64, true>(p, maps, num_sms, stream)
-              : launch<64, false>(p, maps, num_sms, stream);
+  return a.D == 128 ? launch_mode<128>(mode, p, maps, num_sms, stream)
+                    : launch_mode<64>(mode, p, maps, num_sms, stream);
 }
 
 }  // namespace ksa
