@@ -53,7 +53,7 @@ constexpr int kPartsPerSm = 3;  // parts of split items, at most, per SM: the wo
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLead = 4, kLag = 10;  // stagger of the weights' loop, in pairs of keys
 constexpr float kRescale = 8.f;      // log2 of the largest weight before m moves
-constexpr int kCtlBytes = 3072;
+constexpr int kCtlBytes = 3 * 1024;
 
 enum Mode { kPair, kOne, kFew };
 
@@ -851,7 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = 0u;
 #pragma unroll
-            for (int i = 16; i < kKeys / 2; i += 16) tmem_store16(ts + (col0 / 2 + i) % (kKeys / 2), x);
+            for (int i = 16; i < kKeys / 2; i += 16)
+              tmem_store16(ts + (col0 / 2 + i) % (kKeys / 2), x);
           }
           // a pair's scale, exponential, and sum and rounding run staggered, so that the
           // exponential unit (8 cycles a warp instruction) does not wait for them
@@ -874,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum[d & 1] = add2(sum[d & 1], f32x2(p0, p1));
               x[d & 15] = pack_bf16x2(p0, p1);
               if ((d & 15) == 15) tmem_store16(ts + col0 / 2 + (d & ~15), x);
-              if (!FEW && d == kKeys / 4 - 1) {  // the first half of the weights: their products may start
+              if (!FEW && d == kKeys / 4 - 1) {  // half of the weights: their products may start
                 tmem_wait_st();
                 tmem_fence_before();
                 __syncwarp();
