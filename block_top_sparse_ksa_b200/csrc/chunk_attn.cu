@@ -133,7 +133,7 @@ __device__ __forceinline__ void store_32(void *dst, const uint32_t *x) {
                : "memory");
 }
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }  // a <= 2^30
 
 // ---------------------------------------------------------------------------
 // the work warp: rows -> items -> parts
@@ -307,7 +307,8 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
   uint32_t turn = 1;
   while (true) {
     int sum = __shfl_sync(0xffffffffu, units_end, 31);
-    while (id >= first + sum && base + 32 < a.B) {
+    // (rows that overlap by a bad cu_q could count past 2^31: no more work from 2^30 on)
+    while (id >= first + sum && base + 32 < a.B && first < (1 << 30)) {
       first += sum;
       first_slot += __shfl_sync(0xffffffffu, slots_end, 31);
       base += 32;

@@ -827,6 +827,8 @@ ksa_status check_page_call(const ksa_shape *shape, const void *block_table, int3
   if (static_cast<long long>(max_blocks) * shape->block_size != shape->capacity)
     return fail(KSA_ERR_INVALID_ARG, "capacity %d must equal max_blocks * block_size (%d * %d)",
                 shape->capacity, max_blocks, shape->block_size);
+  if (shape->capacity > (1 << 30))
+    return fail(KSA_ERR_UNSUPPORTED, "capacity must be <= 2^30");
   if (!aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(num_free, 4))
     return fail(KSA_ERR_INVALID_ARG, "block_table, free_pages and num_free must be aligned");
   if (ws == nullptr || ws_bytes < 256 || !aligned(ws, 256))
@@ -1054,6 +1056,8 @@ ksa_status check_chunk(const ksa_shape *shape, bool paged, int32_t num_tokens) {
   ksa_status st = check_shape(shape, paged);
   if (st != KSA_OK) return st;
   if (num_tokens < 0) return fail(KSA_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (shape->capacity > (1 << 30))
+    return fail(KSA_ERR_UNSUPPORTED, "capacity must be <= 2^30");
   if (shape->num_q_heads / shape->num_kv_heads > 128)
     return fail(KSA_ERR_UNSUPPORTED, "more than 128 query heads per kv-head");
   if (static_cast<long long>(num_tokens) * shape->num_q_heads >= (1LL << 31))

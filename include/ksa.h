@@ -429,8 +429,9 @@ ksa_status ksa_sparse_decode_attn_noalloc(const ksa_shape *shape, const uint16_t
  *                "Workspaces"); both page calls may share it
  * seq_lens may be ctx_lens and num_free_out may be num_free (a loop that
  * carries its lengths in place); no other overlap.  num_tokens may be 0
- * (slots and positions are then not used).  Only batch, capacity and
- * block_size of the shape matter.  One launch.
+ * (slots and positions are then not used).  Every page belongs to one row.
+ * Only batch, capacity (at most 2^30) and block_size of the shape matter.  One
+ * launch.
  */
 ksa_status ksa_assign_pages(const ksa_shape *shape, const int32_t *ctx_lens,
                             const int32_t *new_lens, int32_t *block_table, int32_t max_blocks,
@@ -545,7 +546,7 @@ ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens
  * clamped and flagged KSA_FLAG_SEQ_LEN_CLAMPED; num_tokens = 0 does nothing.
  * One launch of one CTA per SM; the lengths are read on the device, so a
  * captured call follows them.  The results do not depend on timing.
- * Limits: D in {64, 128}; G <= 128.
+ * Limits: D in {64, 128}; G <= 128; T <= 2^30.
  */
 enum { KSA_MASK_NONE = 0, KSA_MASK_CAUSAL = 1 };
 size_t ksa_chunk_attn_workspace(const ksa_shape *shape, int32_t num_tokens);

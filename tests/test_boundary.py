@@ -386,6 +386,8 @@ def test_validation_of_page_assignment_and_release(ksa):
         assert assign(**kw) == 1, kw
         assert ksa.ksa_last_error() != ""
     assert assign(sh=_shape(ksa, bs=8)) == 2
+    far = (1 << 26) + 1  # blocks of 16: 2^30 + 16 tokens
+    assert assign(sh=_shape(ksa, B=1, Hq=1, Hkv=1, T=far * 16), mb=far) == 2
     for kw in (dict(ws=None), dict(wsb=255), dict(ws=ctypes.c_void_p(0x1010))):
         assert assign(**kw) == 3, kw
 
@@ -477,6 +479,7 @@ def test_validation_of_chunk_attention(ksa):
     assert call(sh=_shape(ksa, D=96)) == 2
     assert call(paged=True, sh=_shape(ksa, bs=8)) == 2
     assert call(n=1 << 30) == 2
+    assert call(sh=_shape(ksa, B=1, Hq=1, Hkv=1, T=(1 << 30) + 1), qs=128) == 2
     assert call(n=0, q=None) == 0
     bad = _shape(ksa, D=96)
     assert lib.ksa_chunk_attn_workspace(ctypes.byref(bad), 7) == 0
