@@ -816,6 +816,8 @@ def _extra(t, dev: int):
         return None
     if _device_of(t, "dev_status") != dev:
         raise ValueError(f"dev_status is on {t.device}, not cuda:{dev}")
+    if t.numel() * t.element_size() < 4:
+        raise ValueError("dev_status must hold a 32-bit word")
     return t.data_ptr()
 
 
@@ -830,15 +832,25 @@ def _scratch(ws: Optional[torch.Tensor], need: int, dev: int):
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _run_on(dev: int, stream, fn, *args) -> None:
-    """One library call on device `dev`, on `stream` or that device's current stream."""
+def _using(stream, dev: int):
+    """The context of a call on another stream than the current one: what the call allocates
+    (workspace, outputs) belongs to that stream, and its zeros are written there."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+        stream = (torch.cuda.ExternalStream(handle, device=dev) if handle != 0
+                  else torch.cuda.default_stream(dev))
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, not cuda:{dev}")
+    return torch.cuda.stream(stream)
+
+
+def _run_on(dev: int, fn, *args) -> None:
+    """One library call on device `dev`, on that device's current stream."""
     if dev == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
-                else _stream(stream))
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
-                    else _stream(stream))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != 0:
         _check(st)
 
@@ -857,6 +869,11 @@ def ksa_assign_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     blocks' pages, taken off the top of the stack free_pages [num_pages]; num_free [1] is
     updated in place unless num_free_out is given.  seq_lens may be ctx_lens."""
     dev = _device_of(block_table, "block_table")
+    if stream is not None:
+        with _using(stream, dev):
+            return ksa_assign_pages(ctx_lens, new_lens, block_table, free_pages, num_free,
+                                    block_size, num_tokens, num_free_out, seq_lens, cu_new, slots,
+                                    positions, workspace, dev_status)
     i32 = torch.int32
     B, mb = block_table.shape
     if num_free_out is None:
@@ -872,7 +889,7 @@ def ksa_assign_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     pages = free_pages.numel()
     ws, ws_ptr, ws_bytes = _scratch(workspace, 256, dev)
     sh = Shape(B, 1, 1, 64, mb * block_size, block_size)
-    _run_on(dev, stream, lib().ksa_assign_pages, ctypes.byref(sh),
+    _run_on(dev, lib().ksa_assign_pages, ctypes.byref(sh),
             _vec(ctx_lens, "ctx_lens", i32, B, dev),
             _vec(new_lens, "new_lens", i32, B, dev),
             _arg(block_table, "block_table", i32, (B, mb), dev), mb, pages,
@@ -894,12 +911,16 @@ def ksa_release_pages(seq_lens: torch.Tensor, done: torch.Tensor, block_table: t
     """Rows with done[b] != 0 give their pages back to the stack (free_pages, num_free); their
     table entries become -1 and their seq_lens 0, all in place."""
     dev = _device_of(block_table, "block_table")
+    if stream is not None:
+        with _using(stream, dev):
+            return ksa_release_pages(seq_lens, done, block_table, free_pages, num_free,
+                                     block_size, workspace, dev_status)
     i32 = torch.int32
     B, mb = block_table.shape
     pages = free_pages.numel()
     ws, ws_ptr, ws_bytes = _scratch(workspace, 256, dev)
     sh = Shape(B, 1, 1, 64, mb * block_size, block_size)
-    _run_on(dev, stream, lib().ksa_release_pages, ctypes.byref(sh),
+    _run_on(dev, lib().ksa_release_pages, ctypes.byref(sh),
             _vec(done, "done", i32, B, dev), _vec(seq_lens, "seq_lens", i32, B, dev),
             _arg(block_table, "block_table", i32, (B, mb), dev), mb, pages,
             _vec(free_pages, "free_pages", i32, pages, dev),
@@ -965,6 +986,10 @@ def _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged, dev_st
         raise ValueError("q needs a Rotary")
     lead = q if q is not None else k
     dev = _device_of(lead, "q" if q is not None else "k")
+    if stream is not None:
+        with _using(stream, dev):
+            return _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged,
+                                  dev_status, None)
     N, Hq, D = lead.shape
     qs = os_ = ks = vs = num_pages = 0
     q_ptr = o_ptr = k_ptr = v_ptr = K_ptr = V_ptr = pos_ptr = slot_ptr = None
@@ -979,8 +1004,8 @@ def _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged, dev_st
         raise ValueError("q_out without q")
     Hkv, B, T, bs = Hq, 1, 1, 16
     if kv:
-        if K.dim() != 4 or K.shape[3] != D:
-            raise ValueError(f"K and V must be 4-dimensional with {D} dims a head")
+        if not isinstance(K, torch.Tensor) or K.dim() != 4 or K.shape[3] != D:
+            raise ValueError(f"K and V must be 4-dimensional tensors with {D} dims a head")
         cache = K.shape
         B, Hkv, T, _ = cache
         ks = _token_rows(k, "k", dev, (N, Hkv, D))
@@ -1007,10 +1032,10 @@ def _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged, dev_st
     args = (ctypes.byref(sh), N, ref, q_ptr, qs, k_ptr, ks, v_ptr, vs, pos_ptr, slot_ptr, o_ptr,
             os_, K_ptr, V_ptr)
     if paged:
-        _run_on(dev, stream, lib().ksa_rotary_append_kv_paged, *args, num_pages,
+        _run_on(dev, lib().ksa_rotary_append_kv_paged, *args, num_pages,
                 _extra(dev_status, dev))
     else:
-        _run_on(dev, stream, lib().ksa_rotary_append_kv, *args, _extra(dev_status, dev))
+        _run_on(dev, lib().ksa_rotary_append_kv, *args, _extra(dev_status, dev))
     return q_out
 
 
@@ -1049,6 +1074,10 @@ def ksa_chunk_attn_workspace(B: int, Hq: int, Hkv: int, D: int, T: int, num_toke
 def _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse, workspace,
                 dev_status, stream):
     dev = _device_of(q, "q")
+    if stream is not None:
+        with _using(stream, dev):
+            return _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse,
+                               workspace, dev_status, None)
     qs = _token_rows(q, "q", dev)
     N, Hq, D = q.shape
     if not isinstance(K, torch.Tensor) or K.dim() != 4 or K.shape[3] != D:
@@ -1077,9 +1106,9 @@ def _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse, wor
             None if lse is None else _arg(lse, "lse", torch.float32, (N, Hq), dev), ws_ptr,
             ws_bytes, _extra(dev_status, dev))
     if pages is not None:
-        _run_on(dev, stream, lib().ksa_chunk_attn_paged, *head, ctypes.byref(pages), *rest)
+        _run_on(dev, lib().ksa_chunk_attn_paged, *head, ctypes.byref(pages), *rest)
     else:
-        _run_on(dev, stream, lib().ksa_chunk_attn, *head, *rest)
+        _run_on(dev, lib().ksa_chunk_attn, *head, *rest)
     return out, lse
 
 

@@ -817,7 +817,7 @@ namespace {
 // Shape, table and pool of the two page calls.
 ksa_status check_page_call(const ksa_shape *shape, const void *block_table, int32_t max_blocks,
                            int32_t num_pages, const void *free_pages, const void *num_free,
-                           const void *ws, size_t ws_bytes) {
+                           const void *ws, size_t ws_bytes, const void *dev_status) {
   ksa_status st = check_shape(shape, true);
   if (st != KSA_OK) return st;
   if (block_table == nullptr || free_pages == nullptr || num_free == nullptr)
@@ -829,8 +829,10 @@ ksa_status check_page_call(const ksa_shape *shape, const void *block_table, int3
                 shape->capacity, max_blocks, shape->block_size);
   if (shape->capacity > (1 << 30))
     return fail(KSA_ERR_UNSUPPORTED, "capacity must be <= 2^30");
-  if (!aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(num_free, 4))
-    return fail(KSA_ERR_INVALID_ARG, "block_table, free_pages and num_free must be aligned");
+  if (!aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(num_free, 4) ||
+      !aligned(dev_status, 4))
+    return fail(KSA_ERR_INVALID_ARG,
+                "block_table, free_pages, num_free and dev_status must be 4-byte aligned");
   if (ws == nullptr || ws_bytes < 256 || !aligned(ws, 256))
     return fail(KSA_ERR_WORKSPACE, "workspace: 256 bytes, 256-byte aligned, are needed");
   return KSA_OK;
@@ -847,7 +849,7 @@ ksa_status ksa_assign_pages(const ksa_shape *shape, const int32_t *ctx_lens,
                             uint32_t *dev_status, void *stream) {
   return guarded([&]() -> ksa_status {
     ksa_status st = check_page_call(shape, block_table, max_blocks, num_pages, free_pages,
-                                    num_free, ws, ws_bytes);
+                                    num_free, ws, ws_bytes, dev_status);
     if (st != KSA_OK) return st;
     if (ctx_lens == nullptr || new_lens == nullptr || num_free_out == nullptr ||
         seq_lens == nullptr || cu_new == nullptr)
@@ -891,7 +893,7 @@ ksa_status ksa_release_pages(const ksa_shape *shape, const int32_t *done, int32_
                              size_t ws_bytes, uint32_t *dev_status, void *stream) {
   return guarded([&]() -> ksa_status {
     ksa_status st = check_page_call(shape, block_table, max_blocks, num_pages, free_pages,
-                                    num_free, ws, ws_bytes);
+                                    num_free, ws, ws_bytes, dev_status);
     if (st != KSA_OK) return st;
     if (done == nullptr || seq_lens == nullptr)
       return fail(KSA_ERR_INVALID_ARG, "done and seq_lens must be non-NULL");
@@ -974,8 +976,9 @@ ksa_status rotary_common(const ksa_shape *shape, int32_t num_tokens, const ksa_r
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
       !aligned(K, 16) || !aligned(V, 16))
     return fail(KSA_ERR_INVALID_ARG, "q, k, v, q_out, K and V must be 16-byte aligned");
-  if (!aligned(positions, 4) || !aligned(slots, 8))
-    return fail(KSA_ERR_INVALID_ARG, "positions must be 4-byte aligned, slots 8-byte");
+  if (!aligned(positions, 4) || !aligned(slots, 8) || !aligned(dev_status, 4))
+    return fail(KSA_ERR_INVALID_ARG,
+                "positions and dev_status must be 4-byte aligned, slots 8-byte");
   const int64_t q_row = static_cast<int64_t>(shape->num_q_heads) * D,
                 kv_row = static_cast<int64_t>(shape->num_kv_heads) * D;
   if ((q != nullptr && (q_stride < q_row || q_stride % 8 != 0 || q_out_stride < q_row ||
@@ -1088,8 +1091,9 @@ ksa_status chunk_common(const ksa_shape *shape, int32_t num_tokens, const uint16
     return fail(KSA_ERR_INVALID_ARG, "q, K, V, cu_q, seq_lens and out must be non-NULL");
   if (!aligned(q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(out, 16))
     return fail(KSA_ERR_INVALID_ARG, "q, K, V and out must be 16-byte aligned");
-  if (!aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4))
-    return fail(KSA_ERR_INVALID_ARG, "cu_q, seq_lens and lse must be 4-byte aligned");
+  if (!aligned(cu_q, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(dev_status, 4))
+    return fail(KSA_ERR_INVALID_ARG,
+                "cu_q, seq_lens, lse and dev_status must be 4-byte aligned");
   if (q_stride < static_cast<int64_t>(shape->num_q_heads) * shape->head_dim || q_stride % 8 != 0)
     return fail(KSA_ERR_INVALID_ARG,
                 "q_stride must be a multiple of 8 elements that holds the token's heads");

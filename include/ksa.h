@@ -426,7 +426,7 @@ ksa_status ksa_sparse_decode_attn_noalloc(const ksa_shape *shape, const uint16_t
  *   num_free_out [1], seq_lens [B], cu_new [B+1] int32, slots [num_tokens]
  *                int64, positions [num_tokens] int32 (written)
  *   ws:          256 bytes, 256-byte aligned, zero-filled once (see
- *                "Workspaces"); both page calls may share it
+ *                "Workspaces"); both page calls may share it, no other call
  * seq_lens may be ctx_lens and num_free_out may be num_free (a loop that
  * carries its lengths in place); no other overlap.  num_tokens may be 0
  * (slots and positions are then not used).  Every page belongs to one row.
@@ -540,7 +540,8 @@ ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens
  *         (0 is allowed; outside [0, T] is clamped and flagged)
  *   out:  [num_tokens, Hq, D] bf16 dense;  lse: [num_tokens, Hq] fp32, nullable
  *   ws:   ksa_chunk_attn_workspace() bytes, 256-byte aligned, zero-filled once
- *         (see "Workspaces")
+ *         (see "Workspaces"); both forms and all shapes may share it, as far as
+ *         it is large enough for each, but no other operator's calls
  * scale == 0 selects 1/sqrt(D).  Places of q and out that no row covers are
  * left alone.  Entries of cu_q outside [0, num_tokens] or descending are
  * clamped and flagged KSA_FLAG_SEQ_LEN_CLAMPED; num_tokens = 0 does nothing.

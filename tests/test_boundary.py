@@ -509,3 +509,31 @@ def test_serving_calls_refuse_cpu_tensors(ksa):
     with pytest.raises(TypeError, match="block_table must be a CUDA tensor"):
         ksa.ksa_chunk_attn_paged(bf(3, 4, 128), bf(1, 2, 16, 128), bf(1, 2, 16, 128), None,
                                  i32(2), i32(1))
+
+
+def test_serving_calls_refuse_an_unaligned_status_word(ksa):
+    """An atomic on a word that is not 4-byte aligned would fault: refused by every serving
+    call."""
+    lib = ksa.lib()
+    odd = ctypes.c_void_p(0x1002)
+    sh = _shape(ksa, B=2, Hq=4, Hkv=2, D=128, T=64, bs=16)
+    ref, big = ctypes.byref(sh), 1 << 30
+    pages = ksa.Pages(FAKE, 4, 10)
+    rot = ksa.Rotary([1.0] * 64)._ref
+    calls = [
+        lambda s: lib.ksa_assign_pages(ref, FAKE, FAKE, FAKE, 4, 9, FAKE, FAKE, FAKE, 5, FAKE,
+                                       FAKE, FAKE, FAKE, FAKE, big, s, None),
+        lambda s: lib.ksa_release_pages(ref, FAKE, FAKE, FAKE, 4, 9, FAKE, FAKE, FAKE, big, s,
+                                        None),
+        lambda s: lib.ksa_rotary_append_kv(ref, 3, rot, FAKE, 512, FAKE, 256, FAKE, 256, FAKE,
+                                           FAKE, FAKE, 512, FAKE, FAKE, s, None),
+        lambda s: lib.ksa_rotary_append_kv_paged(ref, 3, rot, FAKE, 512, FAKE, 256, FAKE, 256,
+                                                 FAKE, FAKE, FAKE, 512, FAKE, FAKE, 10, s, None),
+        lambda s: lib.ksa_chunk_attn(ref, 7, FAKE, 512, FAKE, FAKE, FAKE, FAKE, 1, 0.0, FAKE,
+                                     None, FAKE, big, s, None),
+        lambda s: lib.ksa_chunk_attn_paged(ref, 7, FAKE, 512, FAKE, FAKE, ctypes.byref(pages),
+                                           FAKE, FAKE, 1, 0.0, FAKE, None, FAKE, big, s, None),
+    ]
+    for call in calls:
+        assert call(odd) == 1
+        assert "dev_status" in ksa.ksa_last_error()

@@ -837,3 +837,38 @@ def test_serving_calls_on_two_streams_at_once(ksa):
     torch.cuda.synchronize()
     for _, _, o in lanes:
         assert torch.equal(o, out)
+
+
+def test_serving_calls_allocate_on_the_stream_they_run_on(ksa):
+    """A call on a stream that is still busy, with the workspace and outputs left to the binding:
+    neither their zeros nor their reuse by the current stream's work may reach it."""
+    rows = [(3, 30000), (2, 10)]
+    cache, q, cu, out, _ = check_attn(ksa, rows, 8, 2, 128, 16, True, True, seed=56)
+    seq = i32([30000, 10])
+    T = cache.table.shape[1] * 16
+    need = ksa.ksa_chunk_attn_workspace(2, 8, 2, 128, T, 5)
+    rng = np.random.default_rng(3)
+    table, free, F, pool = page_state(rng, [5, 0, 70], 8, 16, 9)
+    want = ref_assign([5, 0, 70], [20, 3, 1], table, free, F, 16, 30, 128, pool)
+    tables = [torch.from_numpy(table).to(DEV) for _ in range(2)]
+    args = (i32([5, 0, 70]), i32([20, 3, 1]))
+    stack, num = torch.from_numpy(free).to(DEV), i32([F])
+    side = torch.cuda.Stream()
+    long = torch.empty(1 << 29, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for which, t in zip((side, side.cuda_stream), tables):
+        with torch.cuda.stream(side):
+            for _ in range(40):
+                long.fill_(1)
+        got, _ = cache.call(ksa, q, cu, seq, ksa.MASK_CAUSAL, stream=which)
+        left = torch.full((1,), -7, dtype=torch.int32, device=DEV)
+        torch.cuda.current_stream().synchronize()
+        seq2, cu2, slots, pos = ksa.ksa_assign_pages(*args, t, stack, num, 16, 30,
+                                                     num_free_out=left, stream=which)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+                for n in (need, need, 256, 256, out.numel() * 2)]
+        torch.cuda.current_stream().synchronize()
+        side.synchronize()
+        assert all(int(j.min()) == 255 for j in junk)
+        assert torch.equal(got, out)
+        same_assign((t, left, seq2, cu2, slots, pos, want[6]), want)
