@@ -41,6 +41,10 @@ namespace {
 
 constexpr int kQ = 128;        // query rows of a tile
 constexpr int kKeys = 128;     // key tokens of a tile
+// Keys of a tile whose weights are handed over before the others', so that their products run
+// under the last exponentials (16384 keys, 2368 queries, 32 heads of 128: 96 took 531 us, 64 took
+// 536).
+constexpr int kEarly = 96;
 constexpr int kSoftWarps = 8;  // four per stream
 constexpr int kMmaWarp = 8, kKeyWarp = 9, kWorkWarp = 10, kValueWarp = 11;
 // A thread is launched with 65536 / 384 registers, 168.  The softmax keeps a row of 128 scores
@@ -82,8 +86,8 @@ struct Work {
 
 struct Ctl {  // in shared memory
   uint64_t q_full, q_empty, k_full[8], k_empty[8], v_full[8], v_empty[8];
-  // per stream: scores ready, first half of the weights and all of them ready, product with V done
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+  // per stream: scores ready, first kEarly weights and all of them ready, product with V done
+  uint64_t s_full[2], p_early[2], p_full[2], o_done[2];
   uint64_t work_full[kWork], work_empty[kWork], soft, drain;
   Work work[kWork];
   uint32_t tmem;
@@ -520,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&ctl.s_full[s], 1);
-        mbar_init(&ctl.p_half[s], 4);
+        mbar_init(&ctl.p_early[s], 4);
         mbar_init(&ctl.p_full[s], 4);
         mbar_init(&ctl.o_done[s], 1);
       }
@@ -720,16 +724,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = PAIR ? j == 0 : j < 2;  // of its stream
         for (int i = 0; i < (PAIR ? streams : 1); ++i) {
           const int s = PAIR ? i : j & 1;
-          for (int half = 0; half < 2 && ok; ++half) {
-            ok = wait_bar(half == 0 ? &ctl.p_half[s] : &ctl.p_full[s],
+          for (int part = 0; part < 2 && ok; ++part) {
+            ok = wait_bar(part == 0 ? &ctl.p_early[s] : &ctl.p_full[s],
                           s == 0 ? p_turn[0] : p_turn[1], &ctl.abort);
             if (!ok) break;
             tmem_fence_after();
+            constexpr int kSplit = kEarly / 16, kAll = kKeys / 16;
+            if (part == 0) {
 #pragma unroll
-            for (int e = 0; e < kKeys / 32; ++e) {
-              const int x = half * (kKeys / 32) + e;
-              mma_ts(one, tmem + 2 * kKeys + s * D, tmem + s * kKeys + x * 8,
-                     vd + static_cast<uint64_t>(x * 16 * 128 >> 4), idesc_o, !first || x > 0);
+              for (int x = 0; x < kSplit; ++x)
+                mma_ts(one, tmem + 2 * kKeys + s * D, tmem + s * kKeys + x * 8,
+                       vd + static_cast<uint64_t>(x * 16 * 128 >> 4), idesc_o, !first || x > 0);
+            } else {
+#pragma unroll
+              for (int x = kSplit; x < kAll; ++x)
+                mma_ts(one, tmem + 2 * kKeys + s * D, tmem + s * kKeys + x * 8,
+                       vd + static_cast<uint64_t>(x * 16 * 128 >> 4), idesc_o, true);
             }
           }
           if (!ok) break;
@@ -876,11 +886,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum[d & 1] = add2(sum[d & 1], f32x2(p0, p1));
               x[d & 15] = pack_bf16x2(p0, p1);
               if ((d & 15) == 15) tmem_store16(ts + col0 / 2 + (d & ~15), x);
-              if (!FEW && d == kKeys / 4 - 1) {  // half of the weights: their products may start
+              if (!FEW && d == kEarly / 2 - 1) {  // these weights' products may start
                 tmem_wait_st();
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.p_half[s]);
+                if (lane == 0) mbar_arrive(&ctl.p_early[s]);
               }
             }
           }
@@ -892,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (FEW || !active) mbar_arrive(&ctl.p_half[s]);
+          if (FEW || !active) mbar_arrive(&ctl.p_early[s]);
           mbar_arrive(&ctl.p_full[s]);
         }
       }
