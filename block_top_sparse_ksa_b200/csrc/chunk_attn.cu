@@ -183,6 +183,19 @@ __device__ __forceinline__ Rows sort_rows(const Rows &r) {
           __shfl_sync(0xffffffffu, r.tiles, src), __shfl_sync(0xffffffffu, r.deep, src)};
 }
 
+// In key tiles: what a part costs besides its tiles (its start and end), what it costs more if it
+// is joined, and the last join.  A tile takes 1.8 us in pairs, half of that otherwise; measured
+// joins are 28 us for the 256 rows of a pair and 4 parts, 10 us for a few rows.
+struct Costs {
+  float start, part, join;
+};
+template <Mode MODE>
+__device__ __forceinline__ constexpr Costs costs() {
+  return MODE == kPair ? Costs{2.5f, 1.5f, 12.f}
+         : MODE == kOne ? Costs{5.f, 3.f, 10.f}
+                        : Costs{2.5f, 1.5f, 5.f};
+}
+
 // What is cut: items before `whole` are not, the others into parts of `part` key tiles.
 struct Cut {
   int whole, part;
@@ -190,24 +203,22 @@ struct Cut {
 
 // Lane i < 16 tries all items with the deepest cut into i + 1 parts (lane 15: as many as fill the
 // SMs), lane i >= 16 whole items but for the last round that does not fill the SMs, cut into
-// i - 14 parts; every CTA gets the same answer.  Estimated ends, in key tiles (some 1.8 us): a part
-// costs kStart more for its start and end, kPart again if it is joined, and the last join
-// `join` (measured: 28 us for the 256 rows of a pair and 4 parts, 10 us for a few rows).  Equal
-// items go round by round, unequal ones fill the SMs evenly but for a third of a part.
+// i - 14 parts; every CTA gets the same answer.  Estimated ends, in key tiles of the form (see
+// Costs).  Equal items go round by round, unequal ones fill the SMs evenly but for a third of a
+// part.
 __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first, int TT, int ctas,
-                                          int max_parts, float join) {
-  constexpr float kStart = 2.5f, kPart = 1.5f;
+                                          int max_parts, Costs k) {
   const int lane = threadIdx.x & 31;
   float tiles = 0.f, items = 0.f;
   int deepest = 0;
   Rows r = first;
   for (int base = 0; base < a.B; base += 32) {
     if (base > 0) r = load_rows(a, base, TT, nullptr);
-    const float k = static_cast<float>(r.tiles) * a.Hkv;
+    const float n = static_cast<float>(r.tiles) * a.Hkv;
     // mean depth of the row's groups: from the first group's last token to the last one's
     const int top = a.causal ? ceil_div(max(0, r.L - r.n + min(r.n, TT)), kKeys) : r.deep;
-    items += k;
-    tiles += k * 0.5f * (top + r.deep);
+    items += n;
+    tiles += n * 0.5f * (top + r.deep);
     deepest = max(deepest, r.deep);
   }
 #pragma unroll
@@ -228,10 +239,10 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
     const int deep = first.deep;
 #pragma unroll 4
     for (int b = 0; b < a.B; ++b) {
-      const float k = __shfl_sync(0xffffffffu, own, b);
+      const float m = __shfl_sync(0xffffffffu, own, b);
       const float c = ceilf(__shfl_sync(0xffffffffu, deep, b) * per);
-      parts += k * fmaxf(c, 1.f);
-      if (c > 1.f) joined += k * c;
+      parts += m * fmaxf(c, 1.f);
+      if (c > 1.f) joined += m * c;
     }
   } else {  // all rows as deep as the mean
     const float c = fmaxf(1.f, ceilf(__fdividef(mean, s)));
@@ -240,16 +251,16 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
   }
   float cost;
   if (lane < 16) {
-    const float each = __fdividef(tiles, parts) + kStart + (joined > 0.f ? kPart : 0.f);
-    const float even = (tiles + kStart * parts + kPart * joined) * per_cta;
+    const float each = __fdividef(tiles, parts) + k.start + (joined > 0.f ? k.part : 0.f);
+    const float even = (tiles + k.start * parts + k.part * joined) * per_cta;
     cost = equal ? ceilf(parts * per_cta) * each
-                 : fmaxf(even + 0.35f * min(s, deepest), s + kStart);
-    if (joined > 0.f) cost += join;
+                 : fmaxf(even + 0.35f * min(s, deepest), s + k.start);
+    if (joined > 0.f) cost += k.join;
   } else {
     joined = static_cast<float>(rem) * cuts;
     cost = equal && rem > 0 && n > ctas
-               ? (n / ctas) * (mean + kStart) +
-                     ceilf(joined * per_cta) * (__fdividef(mean, cuts) + kStart + kPart) + join
+               ? (n / ctas) * (mean + k.start) +
+                     ceilf(joined * per_cta) * (__fdividef(mean, cuts) + k.start + k.part) + k.join
                : INFINITY;
   }
   if (joined > max_parts) cost = INFINITY;
@@ -272,13 +283,14 @@ __device__ __forceinline__ int warp_scan(int x) {
   return x;
 }
 
-__device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT, Rows r) {
+__device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT, Rows r,
+                                              Costs k) {
   const ChunkArgs &a = p.a;
   const int lane = threadIdx.x & 31;
   const int ctas = static_cast<int>(gridDim.x);
   uint32_t *status = blockIdx.x == 0 ? a.status : nullptr;
   for (int base = 32; status != nullptr && base < a.B; base += 32) load_rows(a, base, TT, status);
-  Cut cut = choose_cut(a, r, TT, ctas, p.max_parts, TT > p.tq ? 12.f : 5.f);
+  Cut cut = choose_cut(a, r, TT, ctas, p.max_parts, k);
   {  // the choice was an estimate: the workspace must hold the real parts
     float joined = 0.f;
     Rows q = r;
@@ -554,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWorkWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    hand_out_work(p, ctl, TT, rows);
+    hand_out_work(p, ctl, TT, rows, costs<MODE>());
   } else if (warp == kKeyWarp || warp == kValueWarp) {
     // ------------------------------------------------------------ loads
     // Two warps, for a page of 16 tokens takes a copy each, and a warp issues one in some 60
@@ -1085,19 +1097,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// By the rows (tokens times heads of a group) of an average sequence: what fills more than a tile
-// of 128 goes in pairs (both tiles then share their keys' loads), what fits in 32 as kFew.  One
-// token over 200 to 1500 states (32 sequences, 16 heads of 64): 36.5 us as kFew, 45.0 as kOne;
-// 5 tokens over 131000 (32 heads on 8 of 128): 96.6 and 100.3.
-Mode choose_mode(int B, int Hq, int Hkv, int N) {
+// By the rows (tokens times heads of a group) of an average sequence.  What fits in 32 goes as
+// kFew: one token over 200 to 1500 states (32 sequences, 16 heads of 64) 36.5 us, 45.0 as kOne;
+// 5 tokens over 131000 (32 heads on 8 of 128) 96.6 and 100.3.  More than a tile of 128 can go in
+// pairs, whose tiles share their keys' loads, or one by one, in items of half the length:
+//   - by the rounds that the SMs take, at 1.2 of a pair's time for two items (6000 keys, 32 heads
+//     on 8 of 128: 512 tokens 75 us in pairs, 55 one by one; 1216: 147 and 131; 1920: 169 and
+//     189; 4800: 402 and 416);
+//   - at D = 64, where the loads are half as large and twice as many places hold them, over more
+//     than 2048 keys always one by one (16384 keys, 2368 tokens: 488 and 413 us; over 1024 keys
+//     38.9 and 42.7);
+//   - over one key tile the second stream of a single item has no work, so a round costs the same.
+Mode choose_mode(int B, int Hq, int Hkv, int D, int T, int N, int num_sms) {
   const int G = Hq / Hkv;
-  const long long rows = static_cast<long long>(N) * G;
-  return rows > static_cast<long long>(kQ) * B           ? kPair
-         : G <= 32 && rows <= static_cast<long long>(32) * B ? kFew
-                                                           : kOne;
+  const long long rows = static_cast<long long>(N) * G, each = (rows + B - 1) / B;
+  if (each <= 32 && G <= 32) return kFew;
+  if (each <= kQ) return kOne;
+  if (D == 64 && T > 2048) return kOne;
+  const auto rounds = [&](int tile) {
+    return (static_cast<long long>(B) * Hkv * ((each + tile - 1) / tile) + num_sms - 1) / num_sms;
+  };
+  const long long pairs = rounds(2 * kQ), ones = rounds(kQ);
+  return (T <= kKeys ? ones <= pairs : 6 * ones < 10 * pairs) ? kOne : kPair;
 }
-
-int rows_of(Mode mode) { return mode == kPair ? 2 * kQ : mode == kOne ? kQ : 32; }
 
 template <int D, Mode MODE>
 cudaError_t launch(const Params &p, const CUtensorMap *maps, int num_sms, cudaStream_t stream) {
@@ -1125,10 +1147,13 @@ size_t sem_bytes(int max_parts) {
 }  // namespace
 
 // workspace: [0] items handed out, [1] CTAs ended, from byte 256 the parts' semaphores (all zero
-// between calls), then the parts
+// between calls), then the parts, as large as any form of these rows needs (so that fewer tokens
+// never need more)
 size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int N, int num_sms) {
   const int max_parts = kPartsPerSm * num_sms;
-  const size_t rows = rows_of(choose_mode(B, Hq, Hkv, N));
+  const int G = Hq / Hkv;
+  const long long each = (static_cast<long long>(N) * G + B - 1) / B;
+  const size_t rows = each > kQ ? 2 * kQ : each > 32 || G > 32 ? kQ : 32;
   return sem_bytes(max_parts) + static_cast<size_t>(max_parts) * rows * (D + 2) * 4;
 }
 
@@ -1140,7 +1165,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStr
   p.done = p.next + 1;
   p.sem = p.next + 64;
   p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + sem_bytes(p.max_parts));
-  const Mode mode = choose_mode(a.B, a.Hq, a.Hkv, a.N);
+  const Mode mode = choose_mode(a.B, a.Hq, a.Hkv, a.D, a.T, a.N, num_sms);
   p.tq = (mode == kFew ? 32 : kQ) / (a.Hq / a.Hkv);
   p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   const bool paged = a.kv.table != nullptr;

@@ -872,3 +872,28 @@ def test_serving_calls_allocate_on_the_stream_they_run_on(ksa):
         assert all(int(j.min()) == 255 for j in junk)
         assert torch.equal(got, out)
         same_assign((t, left, seq2, cu2, slots, pos, want[6]), want)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,Hq,Hkv,bs,paged", [
+    (128, 32, 8, 16, True), (128, 40, 8, 64, False), (64, 32, 8, 32, True), (64, 40, 8, 16, False)])
+def test_chunk_attn_ragged_in_pairs(ksa, causal, D, Hq, Hkv, bs, paged):
+    """As test_chunk_attn_ragged with so many kv-heads that query tiles go in pairs."""
+    check_attn(ksa, EDGES, Hq, Hkv, D, bs, paged, causal, seed=2 * D + Hq + bs, tail=3)
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv,causal", [
+    ([(64 * 40, 9000)], 32, 8, False),                       # two rounds, then a cut tail
+    ([(300, 12000), (8, 100), (8, 90)], 64, 8, True),        # deep items cut, short ones not
+    ([(0, 50), (700, 6000), (1, 1), (90, 3000)], 32, 8, True)])
+def test_chunk_attn_pairs_cut_and_joined(ksa, rows, Hq, Hkv, causal):
+    check_attn(ksa, rows, Hq, Hkv, 128, 16, True, causal, seed=91 + len(rows))
+
+
+def test_chunk_attn_workspace_of_more_tokens_serves_fewer(ksa):
+    """One workspace, asked for once with the most tokens, for every smaller call of the batch,
+    whatever form it takes."""
+    B, Hq, Hkv, T = 3, 32, 8, 4096
+    for D in (64, 128):
+        sizes = [ksa.ksa_chunk_attn_workspace(B, Hq, Hkv, D, T, n) for n in range(0, 3000, 7)]
+        assert sizes == sorted(sizes)
