@@ -98,7 +98,7 @@ struct Ctl {  // in shared memory
 
 struct Params {
   ChunkArgs a;
-  uint32_t *next, *done;  // items handed out beyond the first of each CTA; CTAs that have ended
+  uint32_t *next, *done;  // items handed out beyond the first of each CTA; CTAs that draw no more
   uint32_t *sem;          // [max_parts] parts finished, at the item's first part
   float *part;            // [max_parts] (m, l) of the rows, then O as [D / 4][rows][4]
   int tq, max_parts;      // tq: query tokens of a tile
@@ -221,13 +221,14 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
     tiles += n * 0.5f * (top + r.deep);
     deepest = max(deepest, r.deep);
   }
+  deepest = __reduce_max_sync(0xffffffffu, deepest);
+  if (deepest < 4) return {0, max(deepest, 1)};
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
     items += __shfl_xor_sync(0xffffffffu, items, off);
   }
-  deepest = __reduce_max_sync(0xffffffffu, deepest);
-  if (deepest < 4 || items == 0.f || items > 1e6f) return {0, max(deepest, 1)};
+  if (items > 1e6f) return {0, deepest};
   const int n = static_cast<int>(items), rem = n % ctas;
   const float mean = __fdividef(tiles, items), per_cta = 1.f / ctas;
   const bool equal = mean >= 0.85f * deepest;
@@ -291,18 +292,20 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
   uint32_t *status = blockIdx.x == 0 ? a.status : nullptr;
   for (int base = 32; status != nullptr && base < a.B; base += 32) load_rows(a, base, TT, status);
   Cut cut = choose_cut(a, r, TT, ctas, p.max_parts, k);
-  {  // the choice was an estimate: the workspace must hold the real parts
+  if (cut.whole == 0) {  // the choice was an estimate: the workspace must hold the real parts
     float joined = 0.f;
     Rows q = r;
     for (int b = 0; b < a.B; b += 32) {
       if (b > 0) q = load_rows(a, b, TT, nullptr);
-      const int c = ceil_div(q.deep, cut.part);
-      joined += c > 1 ? static_cast<float>(q.tiles) * a.Hkv * c : 0.f;
+      if (q.deep > cut.part)
+        joined += static_cast<float>(q.tiles) * a.Hkv * ceil_div(q.deep, cut.part);
     }
+    if (__any_sync(0xffffffffu, joined > 0.f)) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) joined += __shfl_xor_sync(0xffffffffu, joined, off);
-    // (of whole items before a cut tail only the tail counts: at most `rem` items, see above)
-    if (cut.whole == 0 && joined > p.max_parts) cut = {0, a.T};
+      for (int off = 16; off > 0; off >>= 1) joined += __shfl_xor_sync(0xffffffffu, joined, off);
+      // (of whole items before a cut tail only the tail counts: at most `rem` items, see above)
+      if (joined > p.max_parts) cut = {0, a.T};
+    }
   }
   // the current 32 rows: parts [first, first + sum of units), whole items, places of parts to join
   int base = 0, first = 0, first_item = 0, first_slot = 0;
@@ -310,12 +313,18 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
   auto measure = [&]() {
     r = sort_rows(r);
     const int items = r.tiles * a.Hkv, end = warp_scan(items);
-    cuts = max(1, ceil_div(r.deep, cut.part));
-    whole = cuts == 1 ? items : min(max(cut.whole - (first_item + end - items), 0), items);
-    units = whole + (items - whole) * cuts;
-    slots = units - whole;
-    units_end = warp_scan(units);
-    slots_end = warp_scan(slots);
+    cuts = 1;
+    whole = units = items;
+    units_end = end;
+    slots = slots_end = 0;
+    if (__any_sync(0xffffffffu, r.deep > cut.part)) {
+      cuts = max(1, ceil_div(r.deep, cut.part));
+      whole = cuts == 1 ? items : min(max(cut.whole - (first_item + end - items), 0), items);
+      units = whole + (items - whole) * cuts;
+      slots = units - whole;
+      units_end = warp_scan(units);
+      slots_end = warp_scan(slots);
+    }
     first_item += __shfl_sync(0xffffffffu, end, 31);
   };
   measure();
@@ -333,8 +342,6 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
       sum = __shfl_sync(0xffffffffu, units_end, 31);
     }
     const bool end = id >= first + sum;
-    int next = 0;
-    if (!end && lane == 0) next = ctas + static_cast<int>(atomicAdd(p.next, 1u));
     Work w{};
     w.token = -1;
     bool use = true;
@@ -349,9 +356,10 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
       const int uncut = __shfl_sync(0xffffffffu, whole, who);
       const bool is_cut = in_row >= uncut;
       const int item = is_cut ? uncut + (in_row - uncut) / c : in_row;
-      const int tile = tiles - 1 - item / a.Hkv;  // when causal, the deepest first
+      const int group = item < a.Hkv ? 0 : item / a.Hkv;
+      const int tile = tiles - 1 - group;  // when causal, the deepest first
       w.z = is_cut ? (in_row - uncut) % c : 0;
-      w.g = item % a.Hkv;
+      w.g = item - group * a.Hkv;
       w.b = __shfl_sync(0xffffffffu, r.b, who);
       w.token = __shfl_sync(0xffffffffu, r.s0, who) + tile * TT;
       w.tokens = min(TT, n - tile * TT);
@@ -361,7 +369,7 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
       const int all = ceil_div(kend, kKeys), s = is_cut ? cut.part : max(all, 1);
       w.t0 = w.z * s;
       w.nt = min(s, all - w.t0);
-      w.parts = max(1, ceil_div(all, s));
+      w.parts = is_cut ? max(1, ceil_div(all, s)) : 1;
       w.slot = is_cut ? slot0 + (item - uncut) * c : 0;
       use = w.z < w.parts;
     }
@@ -377,8 +385,16 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
         turn ^= 1u;
       }
     }
-    if (end) return;
-    id = __shfl_sync(0xffffffffu, next, 0);
+    if (end) break;
+    // the next item, drawn behind this one's handing out: the first one does not wait for it
+    uint32_t drawn = 0u;
+    if (lane == 0) drawn = atomicAdd(p.next, 1u);
+    id = ctas + static_cast<int>(__shfl_sync(0xffffffffu, drawn, 0));
+  }
+  // no CTA draws any more: the counters go back for the next call
+  if (lane == 0 && atomicAdd(p.done, 1u) == gridDim.x - 1u) {
+    *p.next = 0u;
+    *p.done = 0u;
   }
 }
 
@@ -574,9 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of 64, 200 to 1500 states) took 46.6 us instead of 36.5.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const bool keys = warp == kKeyWarp, paged = a.kv.table != nullptr;
-    const int bs = paged ? a.kv.bs : kKeys, ppt = kKeys / bs;  // boxes of a tile and half
-    const int groups = 32 / ppt;                               // tiles whose ids 32 lanes hold
-    const int box = lane % ppt, half = lane / ppt;
+    const int bs = paged ? a.kv.bs : kKeys, log_bs = __ffs(bs) - 1, log_ppt = 7 - log_bs;
+    const int ppt = 1 << log_ppt;                // boxes of a tile and half
+    const int groups = 32 >> log_ppt;            // tiles whose ids 32 lanes hold
+    const int box = lane & (ppt - 1), half = lane >> log_ppt;
     const int none = static_cast<int>(  // a row past the pool: the box reads as zeros
         paged ? static_cast<long long>(a.kv.num_pages) * a.Hkv * bs
               : static_cast<long long>(a.B) * a.Hkv * a.T);
@@ -608,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t *table =
           paged ? a.kv.table + static_cast<size_t>(w.b) * a.kv.max_blocks : nullptr;
       const int kend = a.causal ? max(0, w.seen + w.tokens - 1) : w.len;
-      const int blocks = ceil_div(kend, bs);
+      const int blocks = (kend + bs - 1) >> log_bs;
       auto load_ids = [&](int group) {  // the page of block (t0 + group * groups) * ppt + lane
         const int j = (w.t0 + group * groups) * ppt + lane;
         return paged && j < blocks && j < a.kv.max_blocks ? __ldg(table + j) : -1;
@@ -936,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (FEW) {  // the row's eight maxima and sums
-        const float own = m;
+        const float own = m, other = ctl.ml[s ^ 1][r].x;
         m = -INFINITY;
         l = 0.f;
 #pragma unroll
@@ -946,7 +963,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 y = ctl.ml[i >> 2][(i & 3) * 32 + lane];
           l += y.x == -INFINITY ? y.y : y.y * fast_exp2((y.x - m) * c);
         }
+        has1 = w.nt > (s ^ 1);
         f0 = own == -INFINITY ? 0.f : fast_exp2((own - m) * c);
+        f1 = other == -INFINITY ? 0.f : fast_exp2((other - m) * c);
       } else if (!PAIR) {
         const float2 y = ctl.ml[s ^ 1][r];
         has1 = w.nt > (s ^ 1);
@@ -974,44 +993,60 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[at] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
       }
       if (FEW) {
-        // the copies and streams add up in shared memory: two sums (of the streams), in four
-        // rounds, in each of which the warps of a stream are at different dims
-        constexpr int kBlock = D / 4;
-        for (int i = 0; i < 4; ++i) {
-          const int block = ((warp + i) & 3) * kBlock;
-          float *sum = sums + s * (D * 32) + block * 32 + lane;
+        // A warp adds up both streams for its copy and half of the dims; then the copies go
+        // together through shared memory, 2 and 3 to 0 and 1, and these to each other by halves.
+        constexpr int kOut = D / 4;  // dims that a thread of copy 0 or 1 writes
+        const int copy = warp & 3;
+        float o[2 * kOut];
 #pragma unroll
-          for (int d = 0; d < kBlock; d += 16) {
-            uint32_t v[16];
-            if (has0) tmem_load16(to + block + d, v);
+        for (int i = 0; i < 2 * kOut; i += 16) {
+          uint32_t v[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = has0 ? __uint_as_float(v[e]) * f0 : 0.f;
-              sum[(d + e) * 32] = i == 0 ? x : sum[(d + e) * 32] + x;
-            }
+          for (int e = 0; e < 16; ++e) o[i + e] = 0.f;
+          if (has0) {
+            tmem_load16(to + dim0 + i, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[i + e] = __uint_as_float(v[e]) * f0;
           }
-          soft_sync();
+          if (has1) {
+            tmem_load16(tmem + lanes + 2 * kKeys + (s ^ 1) * D + dim0 + i, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[i + e] += __uint_as_float(v[e]) * f1;
+          }
         }
+        float *sum = sums + ((copy & 1) * 2 + s) * (2 * kOut * 32) + lane;  // [2][2][D / 2][32]
+        if (copy >= 2)
+#pragma unroll
+          for (int e = 0; e < 2 * kOut; ++e) sum[e * 32] = o[e];
+        soft_sync();
+        if (copy < 2) {
+#pragma unroll
+          for (int e = 0; e < 2 * kOut; ++e) o[e] += sum[e * 32];
+#pragma unroll
+          for (int e = 0; e < kOut; ++e) sum[e * 32] = copy == 0 ? o[kOut + e] : o[e];
+        }
+        soft_sync();
         if (!ok) break;
-        constexpr int kOut = D / 8;  // dims that a thread writes
-        const float *sum = sums + warp * kOut * 32 + lane;
-        float o[kOut];
+        if (copy < 2 && valid) {
+          const float *from = sums + ((copy ^ 1) * 2 + s) * (2 * kOut * 32) + lane;
+          const int dim = dim0 + copy * kOut;
 #pragma unroll
-        for (int e = 0; e < kOut; ++e) o[e] = sum[e * 32] + sum[D * 32 + e * 32];
-        if (valid && split) {
-          float4 *dst =
-              reinterpret_cast<float4 *>(part + 2 * C::kRows) + warp * kOut / 4 * C::kRows + row;
+          for (int e = 0; e < kOut; ++e) o[e] = (copy == 0 ? o[e] : o[kOut + e]) + from[e * 32];
+          if (split) {
+            float4 *dst =
+                reinterpret_cast<float4 *>(part + 2 * C::kRows) + dim / 4 * C::kRows + row;
 #pragma unroll
-          for (int e = 0; e < kOut / 4; ++e)
-            dst[e * C::kRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else if (valid) {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + warp * kOut);
+            for (int e = 0; e < kOut / 4; ++e)
+              dst[e * C::kRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + dim);
 #pragma unroll
-          for (int e = 0; e < kOut / 8; ++e)
-            dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
-                                pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
-                                pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+            for (int e = 0; e < kOut / 8; ++e)
+              dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
+                                  pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                  pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
+                                  pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+          }
         }
       } else if (active) {
 #pragma unroll
@@ -1087,14 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (tid == 0) {
-    if (ctl.abort != 0) {
-      flag_status(a.status, KSA_FLAG_WAIT_TIMEOUT);
-    } else if (atomicAdd(p.done, 1u) == gridDim.x - 1u) {  // every CTA has drawn its last item
-      *p.next = 0u;
-      *p.done = 0u;
-    }
-  }
+  if (tid == 0 && ctl.abort != 0) flag_status(a.status, KSA_FLAG_WAIT_TIMEOUT);
 }
 
 // By the rows (tokens times heads of a group) of an average sequence.  What fits in 32 goes as
