@@ -102,6 +102,7 @@ struct Params {
   uint32_t *sem;          // [max_parts] parts finished, at the item's first part
   float *part;            // [max_parts] (m, l) of the rows, then O as [D / 4][rows][4]
   int tq, max_parts;      // tq: query tokens of a tile
+  int group;              // query heads of a kv-head
   bool wide_out;          // out is 32-byte aligned
 };
 
@@ -425,28 +426,35 @@ struct Take {
   }
 };
 
-// The join of an item's parts, by the softmax warps.  First each row's (m, 1 / l) over the parts,
-// in their order, and its lse.
+// The join of an item's parts, by the softmax warps.  First each row's (m, 1 / l) over the parts
+// and its lse: a row by as many neighbouring lanes as there are threads for (1 to 32), 16 parts in
+// flight by each; the lanes' sums go together in a fixed tree.
 template <int D, Mode MODE>
-__device__ __noinline__ void join_stats(const Params &p, const Work &w, float2 *stats, int TQ,
-                                        int G, float c) {
+__device__ __noinline__ void join_stats(const Params &p, const Work &w, float2 *stats) {
   const ChunkArgs &a = p.a;
+  const int G = p.group, TQ = p.tq;
+  const float c = a.scale * kLog2e;
   constexpr int kRows = Cfg<D, MODE>::kRows;
   constexpr size_t pitch = kRows * (D + 2);
   const float *base = p.part + static_cast<size_t>(w.slot) * pitch;
   const int rows = w.tokens * G, parts = w.parts;
-  for (int rr = threadIdx.x; rr < rows; rr += kSoftWarps * 32) {
+  int lanes = 32;
+  while (lanes > 1 && rows * lanes > kSoftWarps * 32) lanes >>= 1;
+  const int sub = threadIdx.x & (lanes - 1);
+  for (int r0 = 0; r0 < rows; r0 += kSoftWarps * 32 / lanes) {
+    const int rr = r0 + static_cast<int>(threadIdx.x) / lanes;
+    const bool real = rr < rows;
     const int tok = rr / G, hh = rr % G;
     const int row = (MODE == kPair ? (tok / TQ) * kQ + (tok % TQ) * G : tok * G) + hh;
     float m = -INFINITY, l = 0.f;
-    for (int q0 = 0; q0 < parts; q0 += 16) {  // 16 parts in flight
+    for (int q0 = sub; q0 < parts && real; q0 += 16 * lanes) {
       float2 ml[16];
       float up = m;
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         ml[q] = make_float2(-INFINITY, 0.f);
-        if (q0 + q < parts)
-          ml[q] = __ldcg(reinterpret_cast<const float2 *>(base + (q0 + q) * pitch) + row);
+        if (q0 + q * lanes < parts)
+          ml[q] = __ldcg(reinterpret_cast<const float2 *>(base + (q0 + q * lanes) * pitch) + row);
       }
 #pragma unroll
       for (int q = 0; q < 16; ++q) up = fmaxf(up, ml[q].x);
@@ -457,6 +465,14 @@ __device__ __noinline__ void join_stats(const Params &p, const Work &w, float2 *
       for (int q = 0; q < 16; ++q)
         l += ml[q].x == -INFINITY ? ml[q].y : ml[q].y * fast_exp2((ml[q].x - m) * c);
     }
+    for (int off = 1; off < lanes; off *= 2) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, off),
+                  l2 = __shfl_xor_sync(0xffffffffu, l, off), up = fmaxf(m, m2);
+      l = (m == -INFINITY ? l : l * fast_exp2((m - up) * c)) +
+          (m2 == -INFINITY ? l2 : l2 * fast_exp2((m2 - up) * c));
+      m = up;
+    }
+    if (!real || sub != 0) continue;
     stats[rr] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
     if (a.lse != nullptr)
       a.lse[(static_cast<long long>(w.token) + tok) * a.Hq + w.g * G + hh] =
@@ -465,12 +481,15 @@ __device__ __noinline__ void join_stats(const Params &p, const Work &w, float2 *
 }
 
 // ... and the outputs, after the warps have met.  A thread adds up 4 dims of a row at a time, parts
-// in order, 4 parts of 4 such quads in flight: the parts come out of L2, some 700 cycles away.
-template <int D, Mode MODE>
-__device__ __noinline__ void join_outputs(const Params &p, const Work &w, const float2 *stats,
-                                          int TQ, int G, float c) {
+// in order, kParts of kQuads such quads in flight: the parts come out of L2, some 700 cycles away.
+// Few rows have no more than a quad for a thread, and then 16 parts in flight (one token over 40000
+// keys, 4 heads on 1, cut into 105 parts: 53.7 us with 4 parts in flight, 24.4 with 16).
+template <int D, Mode MODE, int kQuads, int kParts>
+__device__ __noinline__ void join_outputs(const Params &p, const Work &w, const float2 *stats) {
   const ChunkArgs &a = p.a;
-  constexpr int kRows = Cfg<D, MODE>::kRows, kThr = kSoftWarps * 32, kQuads = 4;
+  const int G = p.group, TQ = p.tq;
+  const float c = a.scale * kLog2e;
+  constexpr int kRows = Cfg<D, MODE>::kRows, kThr = kSoftWarps * 32;
   constexpr size_t pitch = kRows * (D + 2);
   const float *base = p.part + static_cast<size_t>(w.slot) * pitch;
   const int rows = w.tokens * G, work = rows * (D / 4), parts = w.parts;
@@ -488,11 +507,11 @@ __device__ __noinline__ void join_outputs(const Params &p, const Work &w, const 
       st[i] = stats[rr];
       o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int q0 = 0; q0 < parts; q0 += 4) {
-      float m[4][kQuads];
-      float4 x[4][kQuads];
+    for (int q0 = 0; q0 < parts; q0 += kParts) {
+      float m[kParts][kQuads];
+      float4 x[kParts][kQuads];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kParts; ++q) {
         const size_t off = static_cast<size_t>(min(q0 + q, parts - 1)) * pitch;
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
@@ -501,7 +520,7 @@ __device__ __noinline__ void join_outputs(const Params &p, const Work &w, const 
         }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kParts; ++q) {
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
           const bool none = q0 + q >= parts || m[q][i] == -INFINITY;
@@ -545,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168 && C::kSmem <= 227 * 1024, "");
   const ChunkArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.Hq / a.Hkv, TQ = p.tq, TT = TQ * C::kQTiles;
+  const int G = p.group, TQ = p.tq, TT = TQ * C::kQTiles;
 
   if (warp == kValueWarp) {
     if (lane < 8) {
@@ -594,10 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // of 64, 200 to 1500 states) took 46.6 us instead of 36.5.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const bool keys = warp == kKeyWarp, paged = a.kv.table != nullptr;
-    const int bs = paged ? a.kv.bs : kKeys, log_bs = __ffs(bs) - 1, log_ppt = 7 - log_bs;
-    const int ppt = 1 << log_ppt;                // boxes of a tile and half
-    const int groups = 32 >> log_ppt;            // tiles whose ids 32 lanes hold
-    const int box = lane & (ppt - 1), half = lane >> log_ppt;
+    const int log_bs = paged ? __ffs(a.kv.bs) - 1 : 7, bs = 1 << log_bs;
+    const int ppt = kKeys >> log_bs;          // boxes of a tile and half
+    const int groups = 32 >> (7 - log_bs);    // tiles whose ids 32 lanes hold
+    const int box = lane & (ppt - 1), half = lane >> (7 - log_bs);
     const int none = static_cast<int>(  // a row past the pool: the box reads as zeros
         paged ? static_cast<long long>(a.kv.num_pages) * a.Hkv * bs
               : static_cast<long long>(a.B) * a.Hkv * a.T);
@@ -1107,10 +1126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (ctl.last) {
           __threadfence();
-          join_stats<D, MODE>(p, w, &ctl.ml[0][0], TQ, G, c);
+          join_stats<D, MODE>(p, w, &ctl.ml[0][0]);
           soft_sync();
           if (!ok) break;
-          join_outputs<D, MODE>(p, w, &ctl.ml[0][0], TQ, G, c);
+          if (w.tokens * G * (D / 4) <= kSoftWarps * 32)
+            join_outputs<D, MODE, 1, 16>(p, w, &ctl.ml[0][0]);
+          else
+            join_outputs<D, MODE, 4, 4>(p, w, &ctl.ml[0][0]);
           soft_sync();  // before the statistics' place is used again
           if (!ok) break;
         }
@@ -1198,14 +1220,15 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStr
   p.sem = p.next + 64;
   p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + sem_bytes(p.max_parts));
   const Mode mode = choose_mode(a.B, a.Hq, a.Hkv, a.D, a.T, a.N, num_sms);
-  p.tq = (mode == kFew ? 32 : kQ) / (a.Hq / a.Hkv);
+  p.group = a.Hq / a.Hkv;
+  p.tq = (mode == kFew ? 32 : kQ) / p.group;
   p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   const bool paged = a.kv.table != nullptr;
   const uint64_t rows = paged ? static_cast<uint64_t>(a.kv.num_pages) * a.Hkv * a.kv.bs
                               : static_cast<uint64_t>(a.B) * a.Hkv * a.T;
   const int box = paged ? a.kv.bs : kKeys;
   CUtensorMap maps[3];
-  if (!encode_q_tensor_map(&maps[0], a.q, a.D, a.Hq, a.N, a.q_stride, a.Hq / a.Hkv, p.tq) ||
+  if (!encode_q_tensor_map(&maps[0], a.q, a.D, a.Hq, a.N, a.q_stride, p.group, p.tq) ||
       !encode_kv_tensor_map(&maps[1], a.K, rows, a.D, box) ||
       !encode_kv_tensor_map(&maps[2], a.V, rows, a.D, box))
     return cudaErrorInvalidValue;
