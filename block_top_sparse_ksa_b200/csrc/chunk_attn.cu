@@ -11,10 +11,11 @@
 // (P then stays below 2^8 and l and O far inside fp32), so O is rescaled a few
 // times per row and not once per tile; the quotient O / l does not depend on m.
 //
-// Layout.  One CTA per SM holds two streams, each with its S (whose first half
-// P overwrites) and O in tensor memory (2 x (128 + D) of 512 columns) and four
-// softmax warps of one row per thread: no shuffles.  While one stream's softmax
-// runs, the tensor cores work for the other.
+// Layout.  One CTA per SM holds two streams, each with its S and O in tensor
+// memory (2 x (128 + D) of 512 columns; P overwrites the first half of S, or has
+// columns of its own as kOne at D = 64) and four softmax warps of one row per
+// thread: no shuffles.  While one stream's softmax runs, the tensor cores work
+// for the other.
 //   kPair  the streams are two query tiles over the same key tiles.
 //   kOne   one query tile over the even and the odd key tiles, joined at the end.
 //   kFew   as kOne with 32 query rows, four times in the tile: warp w of a stream
@@ -64,6 +65,13 @@ enum Mode { kPair, kOne, kFew };
 template <int D, Mode MODE>
 struct Cfg {
   static constexpr bool kPairs = MODE == kPair, kFews = MODE == kFew;
+  // At D = 64 tensor memory has room for weights beside the scores, so that a stream's next scores
+  // are made while it weighs these.  6000 keys, 32 heads on 8, 2368 queries: 171 -> 163 us, 4800:
+  // 346 -> 336; pairs (39 -> 40 over 1024 keys) and few rows (31.2 -> 31.6 us, 32 sequences of one
+  // token) lose by it.
+  static constexpr bool kApart = D == 64 && MODE == kOne;
+  static constexpr int kWeights = kApart ? 2 * kKeys + 2 * D : 0;  // column of the weights,
+  static constexpr int kPitch = kApart ? kKeys / 2 : kKeys;        // and of stream 1's behind it
   static constexpr int kQBytes = kQ * D * 2, kTileBytes = kKeys * D * 2;  // of Q, of K or V
   static constexpr int kQTiles = kPairs ? 2 : 1;
   static constexpr int kSumBytes = kFews ? 2 * D * 32 * 4 : 0;  // of the copies' sum, [2][D][32]
@@ -86,8 +94,9 @@ struct Work {
 
 struct Ctl {  // in shared memory
   uint64_t q_full, q_empty, k_full[8], k_empty[8], v_full[8], v_empty[8];
-  // per stream: scores ready, first kEarly weights and all of them ready, product with V done
-  uint64_t s_full[2], p_early[2], p_full[2], o_done[2];
+  // per stream: scores ready, scores read, first kEarly weights and all of them ready, product with
+  // V done
+  uint64_t s_full[2], s_free[2], p_early[2], p_full[2], o_done[2];
   uint64_t work_full[kWork], work_empty[kWork], soft, drain;
   Work work[kWork];
   uint32_t tmem;
@@ -553,13 +562,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap v_map,
                       const __grid_constant__ Params p) {
   using C = Cfg<D, MODE>;
-  constexpr bool PAIR = C::kPairs, FEW = C::kFews;
+  constexpr bool PAIR = C::kPairs, FEW = C::kFews, APART = C::kApart;
   constexpr int NK = C::kKeyPlaces, NV = C::kValuePlaces;
   constexpr int A = PAIR ? 1 : 2;  // key tiles whose scores are in use
   extern __shared__ __align__(1024) uint8_t tiles[];
   uint8_t *k_ring = tiles + C::kQTiles * C::kQBytes, *v_ring = k_ring + NK * C::kTileBytes;
   float *sums = reinterpret_cast<float *>(v_ring + NV * C::kTileBytes);
   Ctl &ctl = *reinterpret_cast<Ctl *>(v_ring + NV * C::kTileBytes + C::kSumBytes);
+  static_assert(C::kWeights + 2 * C::kPitch <= 512, "");
   static_assert(sizeof(Ctl) <= kCtlBytes && NK >= 2 && NV <= 8 && NK < kBadRing, "");
   static_assert(2 * kSoftRegs + kOtherRegs <= 3 * 168 && C::kSmem <= 227 * 1024, "");
   const ChunkArgs &a = p.a;
@@ -574,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.v_empty[lane], 1);
     } else if (lane < 10) {
       mbar_init(&ctl.s_full[lane - 8], 1);
+      mbar_init(&ctl.s_free[lane - 8], 4);
       mbar_init(&ctl.p_early[lane - 8], 4);
       mbar_init(&ctl.p_full[lane - 8], 4);
       mbar_init(&ctl.o_done[lane - 8], 1);
@@ -709,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k_next = 0, v_next = 0;  // next places of the rings, and the parities of their filling
     uint32_t k_turn = 0, v_turn = 0, q_turn = 0;
     uint32_t p_turn[2] = {0, 0};  // parity of each stream's next weights
+    uint32_t f_turn[2] = {0, 0};  // and of the reading of its next scores
     bool ok = true;
     auto next_keys = [&]() {  // waits for the next key tile: its place
       const int st = k_next;
@@ -755,6 +767,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < w.nt && ok; ++j) {
         const int sv = v_next;
         int sk = 0;
+        if (APART) {  // the stream's next scores, as soon as these are read
+          const int s = j & 1;
+          if (j + A < w.nt) {
+            sk = next_keys();
+            ok = ok && wait_bar(&ctl.s_free[s], s == 0 ? f_turn[0] : f_turn[1], &ctl.abort);
+            if (!ok) break;
+            tmem_fence_after();
+            scores(s, sk);
+            if (j + A + 1 == w.nt) mma_commit(one, &ctl.q_empty);
+          }
+          // (scores are read before their weights are ready: a turn not waited for has passed)
+          if (s == 0)
+            f_turn[0] ^= 1u;
+          else
+            f_turn[1] ^= 1u;
+        }
         ok = wait_bar(&ctl.v_full[sv], v_turn, &ctl.abort);
         if (!ok) break;
         if (++v_next == NV) {
@@ -785,12 +813,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (part == 0) {
 #pragma unroll
               for (int x = 0; x < kSplit; ++x)
-                mma_ts(one, tmem + 2 * kKeys + s * D, tmem + s * kKeys + x * 8,
+                mma_ts(one, tmem + 2 * kKeys + s * D, tmem + C::kWeights + s * C::kPitch + x * 8,
                        vd + static_cast<uint64_t>(x * 16 * 128 >> 4), idesc_o, !first || x > 0);
             } else {
 #pragma unroll
               for (int x = kSplit; x < kAll; ++x)
-                mma_ts(one, tmem + 2 * kKeys + s * D, tmem + s * kKeys + x * 8,
+                mma_ts(one, tmem + 2 * kKeys + s * D, tmem + C::kWeights + s * C::kPitch + x * 8,
                        vd + static_cast<uint64_t>(x * 16 * 128 >> 4), idesc_o, true);
             }
           }
@@ -801,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p_turn[1] ^= 1u;
           mma_commit(one, &ctl.o_done[s]);
           if (!PAIR || s == streams - 1) mma_commit(one, &ctl.v_empty[sv]);
-          if (j + A < w.nt) {
+          if (!APART && j + A < w.nt) {
             if (i == 0) sk = next_keys();
             if (!ok) break;
             tmem_fence_after();
@@ -826,6 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale * kLog2e;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kKeys, to = tmem + lanes + 2 * kKeys + s * D;
+    const uint32_t tp = tmem + lanes + C::kWeights + s * C::kPitch;
     uint32_t turn = 0, soft_turn = 0;  // parities of the stream's next scores, of the sync below
     int mark = 0;                      // page marks of the item's first key tile
     bool ok = true;
@@ -866,6 +895,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kCols; i += 64) tmem_load64(ts + i, v + i);
           }
+          if (APART) {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.s_free[s]);
+          }
           const int lim = end - j * kKeys - col0;
           const uint32_t bad = ctl.bad[(mark + j) % kBadRing];
           if (lim < kCols) {
@@ -889,6 +923,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]),
                                      max3_nan(mx[6], mx[7], -INFINITY));
           if (!(top < INFINITY)) l = NAN;  // a NaN or infinite score: so is the row's softmax
+          if (APART && k > 0) {  // the last product reads the weights and adds to O
+            ok = wait_bar(&ctl.o_done[s], turn, &ctl.abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tmem_fence_after();
+          }
           if (k == 0) {
             m = top;
           } else if (__any_sync(0xffffffffu, (top - m) * c > kRescale)) {
@@ -896,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = up == -INFINITY ? 1.f : fast_exp2((m - up) * c);
             m = up;
             l *= f;
-            // (the scores' product was issued behind the last one into O, so that one is done)
+            // (the last product into O is done: see above, or these scores' was issued behind it)
 #pragma unroll
             for (int i = 0; i < D; i += 32) {
               uint32_t o[32];
@@ -915,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i) x[i] = 0u;
 #pragma unroll
             for (int i = 16; i < kKeys / 2; i += 16)
-              tmem_store16(ts + (col0 / 2 + i) % (kKeys / 2), x);
+              tmem_store16(tp + (col0 / 2 + i) % (kKeys / 2), x);
           }
           // a pair's scale, exponential, and sum and rounding run staggered, so that the
           // exponential unit (8 cycles a warp instruction) does not wait for them
@@ -937,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float p0 = __uint_as_float(v[2 * d]), p1 = __uint_as_float(v[2 * d + 1]);
               sum[d & 1] = add2(sum[d & 1], f32x2(p0, p1));
               x[d & 15] = pack_bf16x2(p0, p1);
-              if ((d & 15) == 15) tmem_store16(ts + col0 / 2 + (d & ~15), x);
+              if ((d & 15) == 15) tmem_store16(tp + col0 / 2 + (d & ~15), x);
               if (!FEW && d == kEarly / 2 - 1) {  // these weights' products may start
                 tmem_wait_st();
                 tmem_fence_before();
@@ -950,10 +990,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           f32x2_split(add2(sum[0], sum[1]), l0, l1);
           l += l0 + l1;
           tmem_wait_st();
+        } else if (APART && k > 0) {  // nor may a warp without rows be a step ahead of the others
+          ok = wait_bar(&ctl.o_done[s], turn, &ctl.abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) {
+          if (APART && !active) mbar_arrive(&ctl.s_free[s]);
           if (FEW || !active) mbar_arrive(&ctl.p_early[s]);
           mbar_arrive(&ctl.p_full[s]);
         }
