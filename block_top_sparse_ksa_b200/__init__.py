@@ -23,6 +23,11 @@ from typing import Optional
 import numpy as np
 import torch
 
+try:
+    from . import _marshal  # built beside libksa.so; without it every call goes the long way
+except ImportError:
+    _marshal = None
+
 __all__ = [
     "KsaError", "Shape", "lib", "library_path", "ksa_build_block_summaries",
     "ksa_select_blocks", "ksa_sparse_decode_attn", "ksa_unified_select",
@@ -153,6 +158,10 @@ _SIGS = {
 }
 
 _LIB: Optional[ctypes.CDLL] = None
+# addresses of the entry points that _marshal calls, once the library is loaded
+_SHORT = ("ksa_assign_pages", "ksa_release_pages", "ksa_rotary_append_kv",
+          "ksa_rotary_append_kv_paged", "ksa_chunk_attn", "ksa_chunk_attn_paged")
+_ENTRIES: dict = {}
 
 
 def lib() -> ctypes.CDLL:
@@ -168,6 +177,9 @@ def lib() -> ctypes.CDLL:
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
+        if _marshal is not None:
+            for name in _SHORT:
+                _ENTRIES[name] = ctypes.cast(getattr(handle, name), ctypes.c_void_p).value
         _LIB = handle
     return _LIB
 
@@ -772,7 +784,10 @@ def ksa_select_tokens_one_head(q: torch.Tensor, K: torch.Tensor, seq_lens: torch
 
 
 # These calls are made several times per layer and step, some of them for a few microseconds of
-# GPU work, so an argument is checked in one expression and looked at closely only if that fails.
+# GPU work.  With every output and the workspace given, on the current device and stream, they go
+# the short way: csrc/marshal.cpp checks the arguments and calls the library (None: something does
+# not match).  Otherwise an argument is checked in one expression here, and looked at closely only
+# if that fails.
 
 
 def _device_of(t, name: str) -> int:
@@ -868,6 +883,13 @@ def ksa_assign_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table
     [num_tokens] int64, positions [num_tokens]).  block_table [B, max_blocks] gets the new
     blocks' pages, taken off the top of the stack free_pages [num_pages]; num_free [1] is
     updated in place unless num_free_out is given.  seq_lens may be ctx_lens."""
+    if _ENTRIES and stream is None:
+        st = _marshal.assign_pages(_ENTRIES["ksa_assign_pages"], ctx_lens, new_lens, block_table,
+                                   free_pages, num_free, block_size, num_tokens, num_free_out,
+                                   seq_lens, cu_new, slots, positions, workspace, dev_status)
+        if st is not None:
+            _check(st)
+            return seq_lens, cu_new, slots, positions
     dev = _device_of(block_table, "block_table")
     if stream is not None:
         with _using(stream, dev):
@@ -910,6 +932,11 @@ def ksa_release_pages(seq_lens: torch.Tensor, done: torch.Tensor, block_table: t
                       dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows with done[b] != 0 give their pages back to the stack (free_pages, num_free); their
     table entries become -1 and their seq_lens 0, all in place."""
+    if _ENTRIES and stream is None:
+        st = _marshal.release_pages(_ENTRIES["ksa_release_pages"], seq_lens, done, block_table,
+                                    free_pages, num_free, block_size, workspace, dev_status)
+        if st is not None:
+            return _check(st)
     dev = _device_of(block_table, "block_table")
     if stream is not None:
         with _using(stream, dev):
@@ -953,6 +980,7 @@ class Rotary:
             2 * P, self.num_axes, int(bool(interleaved)), self._freq,
             self._axis if self._axis is not None else ctypes.POINTER(ctypes.c_int32)())
         self._ref = ctypes.byref(self._struct)
+        self._address = ctypes.addressof(self._struct)
 
 
 def _token_rows(t: torch.Tensor, name: str, dev: int, shape=None) -> int:
@@ -977,6 +1005,13 @@ def _token_rows(t: torch.Tensor, name: str, dev: int, shape=None) -> int:
 
 
 def _rotary_append(q, k, v, positions, slots, K, V, rotary, q_out, paged, dev_status, stream):
+    if _ENTRIES and stream is None and rotary is not None:
+        st = _marshal.rotary_append(
+            _ENTRIES["ksa_rotary_append_kv_paged" if paged else "ksa_rotary_append_kv"], paged, q,
+            k, v, positions, slots, K, V, rotary._address, q_out, dev_status)
+        if st is not None:
+            _check(st)
+            return q_out
     kv = k is not None
     if kv != (v is not None) or kv != (K is not None) or kv != (V is not None):
         raise ValueError("k, v, K and V must be given together")
@@ -1073,6 +1108,13 @@ def ksa_chunk_attn_workspace(B: int, Hq: int, Hkv: int, D: int, T: int, num_toke
 
 def _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse, workspace,
                 dev_status, stream):
+    if _ENTRIES and stream is None:
+        st = _marshal.chunk_attn(
+            _ENTRIES["ksa_chunk_attn" if block_table is None else "ksa_chunk_attn_paged"], q, K, V,
+            block_table, cu_q, seq_lens, mask, scale, out, lse, workspace, dev_status)
+        if st is not None:
+            _check(st)
+            return out, lse
     dev = _device_of(q, "q")
     if stream is not None:
         with _using(stream, dev):

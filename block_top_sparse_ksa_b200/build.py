@@ -1,4 +1,5 @@
-"""Build libksa.so (the CUDA library behind include/ksa.h) in-tree for sm_100a.
+"""Build libksa.so (the CUDA library behind include/ksa.h) in-tree for sm_100a, and _marshal.so
+(the Python binding's short way to its serving calls, against the installed torch).
 
 Usage: ``python -m block_top_sparse_ksa_b200.build [--force] [--verbose]``.
 nvcc cross-compiles without a GPU; the result sits next to this file so it
@@ -11,10 +12,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libksa.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 # ptxas resource report of the last build (registers, spills, shared memory per kernel)
 REPORT = os.path.join(HERE, "_build", "ptxas.txt")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -34,14 +37,28 @@ def sources():
 def _inputs():
     return (sources() + glob.glob(os.path.join(HERE, "csrc", "*.cuh")) +
             glob.glob(os.path.join(HERE, "csrc", "*.h")) +
+            glob.glob(os.path.join(HERE, "csrc", "*.cpp")) +
             glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _marshal_command():
+    import torch
+    at = os.path.dirname(torch.__file__)
+    include = [os.path.join(ROOT, "include"), os.path.join(at, "include"),
+               os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+               sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            *(f"-I{i}" for i in include), os.path.join(HERE, "csrc", "marshal.cpp"),
+            "-o", MARSHAL + ".tmp", f"-L{os.path.join(at, 'lib')}", "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -49,15 +66,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xptxas=-v", "-Xcompiler", "-fPIC",
            "-shared", "-o", LIB + ".tmp", *sources()]
+    marshal = _marshal_command()
+    beside = subprocess.Popen(marshal, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise subprocess.CalledProcessError(res.returncode, cmd)
+    said = beside.communicate()[0]
+    for code, what, text in ((res.returncode, cmd, res.stdout + res.stderr),
+                             (beside.returncode, marshal, said)):
+        if code != 0:
+            sys.stderr.write(text)
+            raise subprocess.CalledProcessError(code, what)
     if verbose:
         sys.stderr.write(res.stderr)
     os.makedirs(os.path.dirname(REPORT), exist_ok=True)
     with open(REPORT, "w") as f:
         f.write(res.stderr)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

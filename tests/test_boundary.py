@@ -537,3 +537,35 @@ def test_serving_calls_refuse_an_unaligned_status_word(ksa):
     for call in calls:
         assert call(odd) == 1
         assert "dev_status" in ksa.ksa_last_error()
+
+
+def test_short_way_of_the_serving_calls(ksa):
+    """The binding's compiled argument checks are built with the library; what does not match
+    (CPU tensors, missing outputs, wrong types and numbers) is left to the Python checks."""
+    import torch
+    ksa.lib()
+    m = ksa._marshal
+    assert m is not None and set(ksa._ENTRIES) == set(ksa._SHORT) and all(ksa._ENTRIES.values())
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    ws, slots = torch.zeros(256, dtype=torch.uint8), torch.zeros(3, dtype=torch.int64)
+    e = ksa._ENTRIES["ksa_assign_pages"]
+    assign = [e, i32(2), i32(2), i32(2, 4), i32(9), i32(1), 16, 3, None, i32(2), i32(3), slots,
+              i32(3), ws, None]
+    assert m.assign_pages(*assign) is None  # not on a GPU
+    for i in range(len(assign)):
+        for bad in (None, "x", 1 << 40, -1, 0, 2.5, torch.zeros(0)):
+            assert m.assign_pages(*assign[:i], bad, *assign[i + 1:]) is None
+    rot = ksa.Rotary([1.0] * 64)
+    args = [ksa._ENTRIES["ksa_rotary_append_kv"], False, bf(3, 4, 128), bf(3, 2, 128),
+            bf(3, 2, 128), i32(3), slots, bf(1, 2, 8, 128), bf(1, 2, 8, 128), rot._address,
+            bf(3, 4, 128), None]
+    assert m.rotary_append(*args) is None
+    attn = [ksa._ENTRIES["ksa_chunk_attn"], bf(3, 4, 128), bf(1, 2, 8, 128), bf(1, 2, 8, 128),
+            None, i32(2), i32(1), 1, 0.0, bf(3, 4, 128), None, ws, None]
+    assert m.chunk_attn(*attn) is None
+    for f, a in ((m.assign_pages, assign), (m.rotary_append, args), (m.chunk_attn, attn),
+                 (m.release_pages, [None] * 9)):
+        with pytest.raises(TypeError, match="number of arguments"):
+            f(*a[:-1])
+    assert m.release_pages(*[None] * 9) is None

@@ -897,3 +897,92 @@ def test_chunk_attn_workspace_of_more_tokens_serves_fewer(ksa):
     for D in (64, 128):
         sizes = [ksa.ksa_chunk_attn_workspace(B, Hq, Hkv, D, T, n) for n in range(0, 3000, 7)]
         assert sizes == sorted(sizes)
+
+
+def test_serving_calls_by_both_ways(ksa, monkeypatch):
+    """The compiled argument checks and the Python ones make the same calls, and refuse the same
+    arguments with the same errors."""
+    assert ksa._marshal is not None and ksa._ENTRIES
+    N, Hq, Hkv, D, bs = 5, 8, 2, 128, 16
+    qkv = randn((N, (Hq + 2 * Hkv) * D), 1)
+    q, k, v = (x.view(N, -1, D) for x in qkv.split([Hq * D, Hkv * D, Hkv * D], 1))
+    pos3 = torch.arange(3 * N, dtype=torch.int32, device=DEV).view(3, N)
+    rots = [(ksa.Rotary([1.0 / (i + 1) for i in range(64)]), pos3[:1]),
+            (ksa.Rotary([1.0 / (i + 1) for i in range(64)]), pos3[0]),
+            (ksa.Rotary([0.5] * 32, [0] * 10 + [1] * 11 + [2] * 11, interleaved=True), pos3)]
+    both = []
+    for short in (True, False):
+        with monkeypatch.context() as m:
+            calls = []
+            if short:
+                for name in ("assign_pages", "release_pages", "rotary_append", "chunk_attn"):
+                    real = getattr(ksa._marshal, name)
+
+                    def spy(*a, real=real, name=name):
+                        st = real(*a)
+                        calls.append((name, st))
+                        return st
+                    m.setattr(ksa._marshal, name, spy)
+            else:
+                m.setattr(ksa, "_ENTRIES", {})
+            got = []
+            table, free, F, pool = page_state(np.random.default_rng(1), [3, 0], 4, bs, 5)
+            t, stack, num = torch.from_numpy(table).to(DEV), torch.from_numpy(free).to(DEV), i32([F])
+            left, seq, cu = i32([0]), i32([0, 0]), i32([0, 0, 0])
+            slots = torch.zeros(N, dtype=torch.int64, device=DEV)
+            where = torch.zeros(N, dtype=torch.int32, device=DEV)
+            ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+            st = status()
+            for out in (left, None):
+                ksa.ksa_assign_pages(i32([3, 0]), i32([2, 3]), t, stack, num, bs, N,
+                                     num_free_out=out, seq_lens=seq, cu_new=cu, slots=slots,
+                                     positions=where, workspace=ws, dev_status=st)
+                got += [t.clone(), num.clone(), left.clone(), seq.clone(), cu, slots, where]
+            for paged in (True, False):
+                for rot, pos in rots:
+                    K, V = (torch.zeros((pool if paged else 1, Hkv, bs if paged else 64, D),
+                                        dtype=torch.bfloat16, device=DEV) for _ in range(2))
+                    to = torch.zeros((N, Hq, D), dtype=torch.bfloat16, device=DEV)
+                    call = ksa.ksa_rotary_append_kv_paged if paged else ksa.ksa_rotary_append_kv
+                    where2 = slots if paged else torch.arange(N, device=DEV) + 7
+                    assert call(q, k, v, pos, where2, K, V, rot, q_out=to) is to
+                    got += [to, K, V]
+                big = torch.zeros(ksa.ksa_chunk_attn_workspace(2, Hq, Hkv, D, 64, N),
+                                  dtype=torch.uint8, device=DEV)
+                out = torch.zeros((N, Hq, D), dtype=torch.bfloat16, device=DEV)
+                lse = torch.zeros((N, Hq), device=DEV)
+                if paged:
+                    pair = ksa.ksa_chunk_attn_paged(q, K, V, t, cu, seq, out=out, lse=lse,
+                                                    workspace=big, dev_status=st)
+                else:
+                    pair = ksa.ksa_chunk_attn(q, K.expand(2, -1, -1, -1).contiguous(),
+                                              V.expand(2, -1, -1, -1).contiguous(), cu, seq,
+                                              ksa.MASK_NONE, 0.5, out, lse, big)
+                assert pair[0] is out and pair[1] is lse
+                got += [out, lse]
+            ksa.ksa_release_pages(seq, i32([1, 0]), t, stack, num, bs, workspace=ws, dev_status=st)
+            got += [seq, t, stack, num, st]
+            if short:  # every one of these calls was made by it
+                assert len(calls) == 2 + 6 + 2 + 1 and all(s == 0 for _, s in calls)
+            errors = []
+            for bad in (lambda: ksa.ksa_assign_pages(i32([3]), i32([2, 3]), t, stack, num, bs, N),
+                        lambda: ksa.ksa_assign_pages(i32([3, 0]), i32([2, 3]), t, stack, num, 8, N,
+                                                     left, seq, cu, slots, where, ws),
+                        lambda: ksa.ksa_assign_pages(i32([3, 0]), i32([2, 3]), t, stack, num, bs,
+                                                     N, left, seq, cu, slots, where, ws[:100]),
+                        lambda: ksa.ksa_chunk_attn(q, K, V, cu, seq[:1], out=out, lse=lse,
+                                                   workspace=big),
+                        lambda: ksa.ksa_chunk_attn(q, K, V, cu[:2], seq[:1], 7, out=out, lse=lse,
+                                                   workspace=big),
+                        lambda: ksa.ksa_rotary_append_kv(q, k, v, pos3[:2], slots, K, V,
+                                                         rots[2][0], q_out=q.contiguous()),
+                        lambda: ksa.ksa_release_pages(seq, seq.cpu(), t, stack, num, bs, ws)):
+                with pytest.raises(Exception) as e:
+                    bad()
+                errors.append((type(e.value), str(e.value)))
+            torch.cuda.synchronize()
+            both.append(([x.clone() for x in got], errors))
+    assert len(both[0][0]) == len(both[1][0])
+    for a, b in zip(*(x[0] for x in both)):
+        assert torch.equal(a, b)
+    assert both[0][1] == both[1][1]
