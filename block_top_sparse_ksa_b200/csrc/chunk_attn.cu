@@ -195,16 +195,16 @@ __device__ __forceinline__ Rows sort_rows(const Rows &r) {
 }
 
 // In key tiles: what a part costs besides its tiles (its start and end), what it costs more if it
-// is joined, and the last join.  A tile takes 1.8 us in pairs, half of that otherwise; measured
-// joins are 28 us for the 256 rows of a pair and 4 parts, 10 us for a few rows.
+// is joined, and the last join: its start, and each of an item's parts (of full tiles).  A tile
+// takes 1.8 us in pairs, half of that otherwise.
 struct Costs {
-  float start, part, join;
+  float start, part, join, each;
 };
 template <Mode MODE>
 __device__ __forceinline__ constexpr Costs costs() {
-  return MODE == kPair ? Costs{2.5f, 1.5f, 12.f}
-         : MODE == kOne ? Costs{5.f, 3.f, 10.f}
-                        : Costs{2.5f, 1.5f, 5.f};
+  return MODE == kPair ? Costs{2.5f, 1.5f, 8.f, 0.8f}
+         : MODE == kOne ? Costs{5.f, 3.f, 7.5f, 0.8f}
+                        : Costs{2.5f, 1.5f, 4.5f, 0.15f};
 }
 
 // What is cut: items before `whole` are not, the others into parts of `part` key tiles.
@@ -215,12 +215,13 @@ struct Cut {
 // Lane i < 16 tries all items with the deepest cut into i + 1 parts (lane 15: as many as fill the
 // SMs), lane i >= 16 whole items but for the last round that does not fill the SMs, cut into
 // i - 14 parts; every CTA gets the same answer.  Estimated ends, in key tiles of the form (see
-// Costs).  Equal items go round by round, unequal ones fill the SMs evenly but for a third of a
-// part.
+// Costs).  Parts of mostly one size go round by round (6 rows of 29 to 60 thousand keys, 42 items:
+// 146, 172, 272 and 330 parts took 120, 191, 137 and 170 us), others fill the SMs evenly but for a
+// third of a part.
 __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first, int TT, int ctas,
                                           int max_parts, Costs k) {
   const int lane = threadIdx.x & 31;
-  float tiles = 0.f, items = 0.f;
+  float tiles = 0.f, items = 0.f, tokens = 0.f;
   int deepest = 0;
   Rows r = first;
   for (int base = 0; base < a.B; base += 32) {
@@ -229,6 +230,7 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
     // mean depth of the row's groups: from the first group's last token to the last one's
     const int top = a.causal ? ceil_div(max(0, r.L - r.n + min(r.n, TT)), kKeys) : r.deep;
     items += n;
+    tokens += n * min(r.n, TT);
     tiles += n * 0.5f * (top + r.deep);
     deepest = max(deepest, r.deep);
   }
@@ -238,16 +240,24 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
   for (int off = 16; off > 0; off >>= 1) {
     tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
     items += __shfl_xor_sync(0xffffffffu, items, off);
+    tokens += __shfl_xor_sync(0xffffffffu, tokens, off);
   }
   if (items > 1e6f) return {0, deepest};
   const int n = static_cast<int>(items), rem = n % ctas;
   const float mean = __fdividef(tiles, items), per_cta = 1.f / ctas;
   const bool equal = mean >= 0.85f * deepest;
-  {  // no cut can win: 32 rows are looked at in 1.3 us less
-    const float even = (tiles + k.start * items) * per_cta;
-    const float uncut = equal ? ceilf(items * per_cta) * (mean + k.start)
-                              : fmaxf(even + 0.35f * deepest, deepest + k.start);
-    if (0.95f * uncut <= even + k.join) return {0, deepest};
+  auto ends = [&](float parts, float extra, float even, float size) {
+    const float one = __fdividef(tiles, parts), rounds = ceilf(parts * per_cta);
+    return equal                ? rounds * (one + extra)
+           : one >= 0.7f * size ? (rounds - 1.f) * (one + extra) + size + extra
+                                : fmaxf(even + 0.35f * size, size + extra);
+  };
+  const float each = k.each * __fdividef(tokens, items * static_cast<float>(TT));
+  {  // no cut can win (a look at 32 rows takes 1.3 us): c parts of the deepest item end at
+     // deepest / c + each c behind their least cost, and that is 2 sqrt(deepest each) or more
+    const float even = (tiles + k.start * items) * per_cta, x = deepest * each;
+    const float least = k.join + fmaxf(even + 2.f * each, k.start + k.part + 2.f * x * rsqrtf(x));
+    if (0.95f * ends(items, k.start, even, deepest) <= least) return {0, deepest};
   }
   const int cuts = lane < 15 ? lane + 1 : lane == 15 ? max(1, ctas / n) : lane - 14;
   const int s = max(2, ceil_div(deepest, cuts));
@@ -255,7 +265,7 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
   if (a.B <= 32) {
     const float own = static_cast<float>(first.tiles) * a.Hkv, per = __fdividef(1.f, s);
     const int deep = first.deep;
-#pragma unroll 4
+#pragma unroll 8
     for (int b = 0; b < a.B; ++b) {
       const float m = __shfl_sync(0xffffffffu, own, b);
       const float c = ceilf(__shfl_sync(0xffffffffu, deep, b) * per);
@@ -267,18 +277,17 @@ __device__ __forceinline__ Cut choose_cut(const ChunkArgs &a, const Rows &first,
     parts = items * c;
     joined = s < deepest ? parts : 0.f;
   }
+  const float last = k.join + each * ceil_div(deepest, s);
   float cost;
   if (lane < 16) {
-    const float each = __fdividef(tiles, parts) + k.start + (joined > 0.f ? k.part : 0.f);
     const float even = (tiles + k.start * parts + k.part * joined) * per_cta;
-    cost = equal ? ceilf(parts * per_cta) * each
-                 : fmaxf(even + 0.35f * min(s, deepest), s + k.start);
-    if (joined > 0.f) cost += k.join;
+    cost = ends(parts, k.start + (joined > 0.f ? k.part : 0.f), even, min(s, deepest));
+    if (joined > 0.f) cost += last;
   } else {
     joined = static_cast<float>(rem) * cuts;
     cost = equal && rem > 0 && n > ctas
                ? (n / ctas) * (mean + k.start) +
-                     ceilf(joined * per_cta) * (__fdividef(mean, cuts) + k.start + k.part) + k.join
+                     ceilf(joined * per_cta) * (__fdividef(mean, cuts) + k.start + k.part) + last
                : INFINITY;
   }
   if (joined > max_parts) cost = INFINITY;
