@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ loads
     // Two warps, for a page of 16 tokens takes a copy each, and a warp issues one in some 60
     // cycles: with one warp, cross attention of one token over pages of 16 (32 sequences, 16 heads
-    // of 64, 200 to 1500 states) took 46.6 us instead of 36.5.
+    // of 64, 200 to 1500 states) took 28% longer.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     const bool keys = warp == kKeyWarp, paged = a.kv.table != nullptr;
     const int log_bs = paged ? __ffs(a.kv.bs) - 1 : 7, bs = 1 << log_bs;
@@ -1206,15 +1206,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // By the rows (tokens times heads of a group) of an average sequence.  What fits in 32 goes as
-// kFew: one token over 200 to 1500 states (32 sequences, 16 heads of 64) 36.5 us, 45.0 as kOne;
-// 5 tokens over 131000 (32 heads on 8 of 128) 96.6 and 100.3.  More than a tile of 128 can go in
+// kFew: one token over 200 to 1500 states (32 sequences, 16 heads of 64) 32 us, 43 as kOne;
+// 5 tokens over 131000 (32 heads on 8 of 128) 96 and 101.  More than a tile of 128 can go in
 // pairs, whose tiles share their keys' loads, or one by one, in items of half the length:
 //   - by the rounds that the SMs take, at 1.2 of a pair's time for two items (6000 keys, 32 heads
-//     on 8 of 128: 512 tokens 75 us in pairs, 55 one by one; 1216: 147 and 131; 1920: 169 and
-//     189; 4800: 402 and 416);
+//     on 8 of 128: 512 tokens 73 us in pairs, 55 one by one; 1216: 130 and 122; 1920: 169 and
+//     172; 4800: 381 and 411);
 //   - at D = 64, where the loads are half as large and twice as many places hold them, over more
-//     than 2048 keys always one by one (16384 keys, 2368 tokens: 488 and 413 us; over 1024 keys
-//     38.9 and 42.7);
+//     than 2048 keys always one by one (16384 keys, 2368 tokens: 474 and 437 us; over 1024 keys
+//     39 and 40);
 //   - over one key tile the second stream of a single item has no work, so a round costs the same.
 Mode choose_mode(int B, int Hq, int Hkv, int D, int T, int N, int num_sms) {
   const int G = Hq / Hkv;
