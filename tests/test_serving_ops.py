@@ -986,3 +986,13 @@ def test_serving_calls_by_both_ways(ksa, monkeypatch):
     for a, b in zip(*(x[0] for x in both)):
         assert torch.equal(a, b)
     assert both[0][1] == both[1][1]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [9, 17, 33, 42, 43, 65, 97])
+def test_chunk_attn_tiles_with_idle_warps(ksa, D, n):
+    """Query tiles that leave some of a stream's warps without rows, over many key tiles, whole
+    and cut: such warps keep step with the others."""
+    check_attn(ksa, [(n, 2300), (n, 1290), (n, 129)], 8, 2, D, 16, True, True, seed=n)
+    check_attn(ksa, [(n, 20011)], 3, 1, D, 32, False, False, seed=n + 1)
+    check_attn(ksa, [(n, 2176)] * 40, 24, 8, D, 64, True, False, seed=n + 2)
