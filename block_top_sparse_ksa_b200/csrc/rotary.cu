@@ -57,6 +57,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int q_heads = a.q != nullptr ? a.Hq : 0;
   const int heads = q_heads + (a.k != nullptr ? 2 * a.Hkv : 0);
   const int items = nt * heads * kPer;
+  // elements between the kv-heads of a row or page (a contiguous row may hold 2^31 and more)
+  const long long head_pitch = static_cast<long long>(a.slots_per_page) * D;
   // first every load that the CTA needs: positions, slots, data
   int pos[kAngles];
 #pragma unroll
@@ -149,8 +151,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       }
       uint16_t *dst =
           g < 0 ? a.q_out + static_cast<long long>(n0 + t[u]) * a.q_out_stride + head[u] * D
-                : (is_v ? a.V : a.K) + at +
-                      static_cast<long long>(is_v ? g - a.Hkv : g) * (a.slots_per_page * D);
+                : (is_v ? a.V : a.K) + at + (is_v ? g - a.Hkv : g) * head_pitch;
       reinterpret_cast<uint4 *>(dst)[clo[u]] = lo[u];
       reinterpret_cast<uint4 *>(dst)[chi[u]] = hi[u];
     }

@@ -371,6 +371,24 @@ def test_rotary_offsets_past_32_bits(ksa):
     assert torch.equal(K[0, :, 0], k[1]) and torch.equal(K[P - 2, :, 7], k[2])
 
 
+@pytest.mark.parametrize("D", [128, 64])
+def test_rotary_heads_past_32_bits(ksa, D):
+    """A contiguous cache whose heads lie more than 2^31 elements apart: the last head's rows land
+    in the last head, and no other row of the cache changes."""
+    Hkv, T = 2, 2 ** 31 // D + 64
+    K, V = (torch.zeros((1, Hkv, T, D), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    k, v = randn((4, Hkv, D), 1), randn((4, Hkv, D), 2)
+    slots = torch.tensor([T - 1, 0, T // 2, -1], device=DEV)
+    st = status()
+    ksa.ksa_rotary_append_kv(None, k, v, None, slots, K, V, None, dev_status=st)
+    assert int(st) == 0
+    for x, src in ((K, k), (V, v)):
+        for n, t in enumerate(slots.tolist()[:3]):
+            assert torch.equal(x[0, :, t], src[n])
+            x[0, :, t] = 0
+        assert not any(bool(part.any()) for part in x.view(-1, D).chunk(16))
+
+
 # ---------------------------------------------------------------------------
 # chunk attention
 
