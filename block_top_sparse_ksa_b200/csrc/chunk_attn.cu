@@ -129,6 +129,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *ab
   return true;
 }
 
+// The same for a whole warp: its lanes leave together, for a lane that goes on alone would wait for
+// the others at the next vote.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *abort) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
+}
+
 // Largest of three, NaN if one is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float r;
@@ -400,7 +406,7 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
       use = w.z < w.parts;
     }
     if (use) {
-      if (!wait_bar(&ctl.work_empty[at], turn, &ctl.abort)) return;
+      if (!warp_wait(&ctl.work_empty[at], turn, &ctl.abort)) return;
       if (lane == 0) {
         ctl.work[at] = w;
         mbar_arrive(&ctl.work_full[at]);
@@ -429,8 +435,7 @@ struct Take {
   int at = 0;
   uint32_t turn = 0;
   __device__ __forceinline__ bool get(Ctl &ctl, Work &w) {
-    const bool ok = wait_bar(&ctl.work_full[at], turn, &ctl.abort);
-    if (!__all_sync(0xffffffffu, ok)) return false;
+    if (!warp_wait(&ctl.work_full[at], turn, &ctl.abort)) return false;
     w = ctl.work[at];
     return true;
   }
@@ -648,8 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t drained = 1, q_turn = 1;  // a place's first filling waits for nothing
     bool ok = true;
     auto load_q = [&](const Work &w) {
-      ok = wait_bar(&ctl.q_empty, q_turn, &ctl.abort);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait(&ctl.q_empty, q_turn, &ctl.abort);
       if (!ok) return;
       q_turn ^= 1u;
       if (lane == 0) {
@@ -696,8 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (bad != 0u) flag_status(a.status, KSA_FLAG_INDEX_SKIPPED);
         }
         mark = (mark + 1) % kBadRing;
-        ok = wait_bar(&empty[stage], drained, &ctl.abort);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(&empty[stage], drained, &ctl.abort);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], C::kTileBytes);
         __syncwarp();
@@ -728,8 +731,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t one = elect_one();
     int k_next = 0, v_next = 0;  // next places of the rings, and the parities of their filling
     uint32_t k_turn = 0, v_turn = 0, q_turn = 0;
-    uint32_t p_turn[2] = {0, 0};  // parity of each stream's next weights
-    uint32_t f_turn[2] = {0, 0};  // and of the reading of its next scores
+    uint32_t p_turn = 0;  // bit s: parity of stream s's next weights
+    uint32_t f_turn = 0;  // and of the reading of its next scores
+    // A vote after each wait would stand between the weights and their products.  So a lane that a
+    // wait has failed waits no more, but stays in step to the item's end, where the warp votes: the
+    // products until then are of no use, and harm nothing.
     bool ok = true;
     auto next_keys = [&]() {  // waits for the next key tile: its place
       const int st = k_next;
@@ -765,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ok && wait_bar(&ctl.q_full, q_turn, &ctl.abort);
           q_turn ^= 1u;
         }
-        if (!ok) break;
         tmem_fence_after();
         if (PAIR)
           for (int s = 0; s < streams; ++s) scores(s, st);
@@ -773,27 +778,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           scores(j, st);
       }
       if (w.nt <= A) mma_commit(one, &ctl.q_empty);
-      for (int j = 0; j < w.nt && ok; ++j) {
+      for (int j = 0; j < w.nt; ++j) {
         const int sv = v_next;
         int sk = 0;
         if (APART) {  // the stream's next scores, as soon as these are read
           const int s = j & 1;
           if (j + A < w.nt) {
             sk = next_keys();
-            ok = ok && wait_bar(&ctl.s_free[s], s == 0 ? f_turn[0] : f_turn[1], &ctl.abort);
-            if (!ok) break;
+            ok = ok && wait_bar(&ctl.s_free[s], (f_turn >> s) & 1u, &ctl.abort);
             tmem_fence_after();
             scores(s, sk);
             if (j + A + 1 == w.nt) mma_commit(one, &ctl.q_empty);
           }
           // (scores are read before their weights are ready: a turn not waited for has passed)
-          if (s == 0)
-            f_turn[0] ^= 1u;
-          else
-            f_turn[1] ^= 1u;
+          f_turn ^= 1u << s;
         }
-        ok = wait_bar(&ctl.v_full[sv], v_turn, &ctl.abort);
-        if (!ok) break;
+        ok = ok && wait_bar(&ctl.v_full[sv], v_turn, &ctl.abort);
         if (++v_next == NV) {
           v_next = 0;
           v_turn ^= 1u;
@@ -813,10 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = PAIR ? j == 0 : j < 2;  // of its stream
         for (int i = 0; i < (PAIR ? streams : 1); ++i) {
           const int s = PAIR ? i : j & 1;
-          for (int part = 0; part < 2 && ok; ++part) {
-            ok = wait_bar(part == 0 ? &ctl.p_early[s] : &ctl.p_full[s],
-                          s == 0 ? p_turn[0] : p_turn[1], &ctl.abort);
-            if (!ok) break;
+          for (int part = 0; part < 2; ++part) {
+            ok = ok && wait_bar(part == 0 ? &ctl.p_early[s] : &ctl.p_full[s],
+                                (p_turn >> s) & 1u, &ctl.abort);
             tmem_fence_after();
             constexpr int kSplit = kEarly / 16, kAll = kKeys / 16;
             if (part == 0) {
@@ -831,22 +830,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                        vd + static_cast<uint64_t>(x * 16 * 128 >> 4), idesc_o, true);
             }
           }
-          if (!ok) break;
-          if (s == 0)
-            p_turn[0] ^= 1u;
-          else
-            p_turn[1] ^= 1u;
+          p_turn ^= 1u << s;
           mma_commit(one, &ctl.o_done[s]);
           if (!PAIR || s == streams - 1) mma_commit(one, &ctl.v_empty[sv]);
           if (!APART && j + A < w.nt) {
             if (i == 0) sk = next_keys();
-            if (!ok) break;
             tmem_fence_after();
             scores(s, sk);
             if (j + A + 1 == w.nt && (!PAIR || s == streams - 1)) mma_commit(one, &ctl.q_empty);
           }
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
     }
     // the tensor memory goes back only when no product runs
     mma_commit(one, &ctl.drain);
@@ -870,8 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto soft_sync = [&]() {  // all softmax warps; with a limit, unlike a named barrier
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.soft);
-      ok = wait_bar(&ctl.soft, soft_turn, &ctl.abort) && ok;
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait(&ctl.soft, soft_turn, &ctl.abort) && ok;
       soft_turn ^= 1u;
     };
     Take take;
@@ -891,8 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < steps; ++k) {
         const int j = PAIR ? k : 2 * k + s;
-        ok = wait_bar(&ctl.s_full[s], turn, &ctl.abort);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = warp_wait(&ctl.s_full[s], turn, &ctl.abort);
         if (!ok) break;
         turn ^= 1u;
         tmem_fence_after();
@@ -933,8 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      max3_nan(mx[6], mx[7], -INFINITY));
           if (!(top < INFINITY)) l = NAN;  // a NaN or infinite score: so is the row's softmax
           if (APART && k > 0) {  // the last product reads the weights and adds to O
-            ok = wait_bar(&ctl.o_done[s], turn, &ctl.abort);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = warp_wait(&ctl.o_done[s], turn, &ctl.abort);
             if (!ok) break;
             tmem_fence_after();
           }
@@ -1000,8 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += l0 + l1;
           tmem_wait_st();
         } else if (APART && k > 0) {  // nor may a warp without rows be a step ahead of the others
-          ok = wait_bar(&ctl.o_done[s], turn, &ctl.abort);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = warp_wait(&ctl.o_done[s], turn, &ctl.abort);
           if (!ok) break;
         }
         tmem_fence_before();
@@ -1022,7 +1013,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float f0 = 1.f, f1 = 0.f;
       bool has0 = steps > 0, has1 = false;
       // every step's product arrives on o_done: the last one's parity is behind `turn`
-      if (steps > 0) ok = wait_bar(&ctl.o_done[s], turn ^ 1u, &ctl.abort);
+      if (steps > 0) ok = warp_wait(&ctl.o_done[s], turn ^ 1u, &ctl.abort);
+      if (PAIR && !ok) break;  // (otherwise behind the join's sync)
       if (!PAIR) {  // join the streams: each half of the warps writes half of the dims
         ctl.ml[s][r] = make_float2(m, l);
         tmem_fence_before();
@@ -1052,8 +1044,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * f0 + y.y * f1;
         m = both;
       }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       tmem_fence_after();
       const bool split = w.parts > 1;
       constexpr int kDims = PAIR ? D : D / 2;  // of this warp

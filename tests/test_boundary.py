@@ -569,3 +569,24 @@ def test_short_way_of_the_serving_calls(ksa):
         with pytest.raises(TypeError, match="number of arguments"):
             f(*a[:-1])
     assert m.release_pages(*[None] * 9) is None
+
+
+def test_chunk_attention_waits_end_for_whole_warps():
+    """A wait that gives up must end for all lanes of its warp alike: the others would wait for
+    ever at the next vote.  So every wait is voted on, except the products warp's, whose lanes stay
+    in step to the item's end (no lane leaves between a wait and the vote there)."""
+    here = os.path.join(ROOT, "block_top_sparse_ksa_b200", "csrc", "chunk_attn.cu")
+    with open(here) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    at = text.rindex("} else if (warp == kMmaWarp) {")
+    products = text[at:text.index("} else if (warp < kSoftWarps) {")]
+    others = text.replace(products, "")
+    # the definition, and warp_wait's call under its vote
+    assert len(re.findall(r"\bwait_bar\(", others)) == 2
+    assert re.search(r"return __all_sync\(0xffffffffu, wait_bar\(bar, parity, abort\)\);", others)
+    assert len(re.findall(r"\bwait_bar\(", products)) == 5
+    assert len(re.findall(r"ok = ok && wait_bar\(", products)) == 5
+    assert "break" not in products and "return false" not in products
+    loops = re.findall(r"(?:for|while) \([^\n]*\bok\b[^\n]*", products)
+    assert loops == ["while (ok && take.get(ctl, w) && w.token >= 0) {"]
+    assert re.search(r"ok = __all_sync\(0xffffffffu, ok\);\s*}\s*mma_commit", products)
