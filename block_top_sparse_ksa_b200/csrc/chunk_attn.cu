@@ -32,6 +32,13 @@
 // items do not fill the SMs evenly, their keys are split into parts of `part`
 // tiles; the last CTA to finish a split item joins the parts in their order, so
 // results do not depend on timing.
+//
+// Long axes.  The tensor cores add to O by cutting bits off: a tile takes up to
+// 5.1e-7 of O away, always towards zero (values of mean 1 over 2^20 keys came out
+// 0.4% low, over 2^24 6%).  So a CTA takes the tiles of an item or part in
+// segments of kSegment (2.6e-4), O begins anew in each, and the segments are
+// added up in fp32 with rounding, in a place of the CTA's in the workspace.  No
+// wait in a CTA is then longer than a segment, about a millisecond.
 #include "ksa_device.cuh"
 #include "ksa_internal.h"
 #include "tcgen05_device.cuh"
@@ -54,6 +61,7 @@ constexpr int kThreads = 384;
 constexpr int kSoftRegs = 224, kOtherRegs = 56;
 constexpr int kBadRing = 32;   // key tiles whose page marks are kept (above any stage count)
 constexpr int kWork = 2;       // items a CTA holds: the one it computes, and the next one
+constexpr int kSegment = 512;  // key tiles that O is summed over in tensor memory, at most
 constexpr int kPartsPerSm = 3;  // parts of split items, at most, per SM: the workspace's size
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLead = 4, kLag = 10;  // stagger of the weights' loop, in pairs of keys
@@ -90,7 +98,10 @@ struct Work {
   int len;           // L of the row
   int t0, nt;        // key tiles of this part
   int parts, slot, z;  // parts of the item, the first part's place in the workspace, this part
+                       // (with kBegun: segments of it come before this one; kMore: behind it)
 };
+
+constexpr int kBegun = 1 << 30, kMore = 1 << 29;  // see Work::z (below 2^29)
 
 struct Ctl {  // in shared memory
   uint64_t q_full, q_empty, k_full[8], k_empty[8], v_full[8], v_empty[8];
@@ -110,6 +121,7 @@ struct Params {
   uint32_t *next, *done;  // items handed out beyond the first of each CTA; CTAs that draw no more
   uint32_t *sem;          // [max_parts] parts finished, at the item's first part
   float *part;            // [max_parts] (m, l) of the rows, then O as [D / 4][rows][4]
+  float *carry;           // [CTAs] (m, l) of the softmax threads, then O, of the segments so far
   int tq, max_parts;      // tq: query tokens of a tile
   int group;              // query heads of a kv-head
   bool wide_out;          // out is 32-byte aligned
@@ -405,7 +417,10 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
       w.slot = is_cut ? slot0 + (item - uncut) * c : 0;
       use = w.z < w.parts;
     }
-    if (use) {
+    const int all = w.nt, z = w.z;
+    for (int done = 0; use; done += kSegment) {
+      w.nt = min(all - done, kSegment);
+      w.z = z | (done > 0 ? kBegun : 0) | (all - done > kSegment ? kMore : 0);
       if (!warp_wait(&ctl.work_empty[at], turn, &ctl.abort)) return;
       if (lane == 0) {
         ctl.work[at] = w;
@@ -416,6 +431,8 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
         at = 0;
         turn ^= 1u;
       }
+      w.t0 += kSegment;
+      use = all - done > kSegment;
     }
     if (end) break;
     // the next item, drawn behind this one's handing out: the first one does not wait for it
@@ -448,6 +465,79 @@ struct Take {
     }
   }
 };
+
+// Floats of a CTA's sums over segments: (m, l) of each softmax thread, then the O that it has.
+__host__ __device__ constexpr size_t carry_floats(int rows, int D) {
+  return 2 * kSoftWarps * 32 + static_cast<size_t>(rows) * D;
+}
+
+// A segment that is not a part's only one, by a softmax warp: the segments before and O of the
+// streams (the warp's own and, but for pairs, the other one; with the weights f0 and f1, 0: none)
+// go together.  If more segments follow, the sum goes to the workspace, else over the warp's own
+// O.  Returns its (m, l).
+template <int D, Mode MODE>
+__device__ __forceinline__ float2 add_segment(const Params &p, const Ctl &ctl, const Work &w,
+                                              float f0, float f1, float2 ml) {
+  constexpr int DIMS = MODE == kPair ? D : D / 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = warp >> 2;
+  const float c = p.a.scale * kLog2e;
+  const uint32_t at = ctl.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 2 * kKeys +
+                      (MODE == kPair ? 0 : s * DIMS);
+  const uint32_t own = at + s * D, other = at + (s ^ 1) * D;
+  float *carry = p.carry + blockIdx.x * carry_floats(kSoftWarps * 32 * DIMS / D, D);
+  float2 *stats = reinterpret_cast<float2 *>(carry) + threadIdx.x;
+  float4 *sums = reinterpret_cast<float4 *>(carry + 2 * kSoftWarps * 32) +
+                 warp * (DIMS / 4 * 32) + lane;  // [warps][DIMS / 4][32]
+  float f = 0.f;  // of the segments before
+  if (w.z & kBegun) {
+    const float2 y = *stats;
+    const float up = fmaxf(ml.x, y.x);
+    const float g = ml.x == -INFINITY ? 1.f : fast_exp2((ml.x - up) * c);
+    f = y.x == -INFINITY ? 0.f : fast_exp2((y.x - up) * c);
+    ml = make_float2(up, ml.y * g + (y.x == -INFINITY ? y.y : y.y * f));
+    f0 *= g;
+    f1 *= g;
+  }
+  if (w.z & kMore) *stats = ml;
+#pragma unroll 1
+  for (int i = 0; i < DIMS; i += 16) {
+    uint32_t v[16];
+    float o[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+    if (__any_sync(0xffffffffu, f0 != 0.f)) {
+      tmem_load16(own + i, v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (f0 != 0.f) o[e] = __uint_as_float(v[e]) * f0;
+    }
+    if (__any_sync(0xffffffffu, f1 != 0.f)) {
+      tmem_load16(other + i, v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (f1 != 0.f) o[e] += __uint_as_float(v[e]) * f1;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (f != 0.f) {
+        const float4 x = sums[(i / 4 + q) * 32];
+        o[4 * q] += x.x * f;
+        o[4 * q + 1] += x.y * f;
+        o[4 * q + 2] += x.z * f;
+        o[4 * q + 3] += x.w * f;
+      }
+      if (w.z & kMore)
+        sums[(i / 4 + q) * 32] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    }
+    if (!(w.z & kMore)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e]);
+      tmem_store16(own + i, v);
+    }
+  }
+  tmem_wait_st();
+  return ml;
+}
 
 // The join of an item's parts, by the softmax warps.  First each row's (m, 1 / l) over the parts
 // and its lse: a row by as many neighbouring lanes as there are threads for (1 to 32), 16 parts in
@@ -1045,10 +1135,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = both;
       }
       tmem_fence_after();
-      const bool split = w.parts > 1;
       constexpr int kDims = PAIR ? D : D / 2;  // of this warp
       const int dim0 = PAIR ? 0 : s * kDims;
-      float *part = p.part + static_cast<size_t>(w.slot + w.z) * (C::kRows * (D + 2));
+      if (w.z >= kMore) {
+        const float2 y =
+            add_segment<D, MODE>(p, ctl, w, has0 ? f0 : 0.f, has1 ? f1 : 0.f, make_float2(m, l));
+        if (w.z & kMore) {
+          tmem_fence_before();
+          if (!PAIR) soft_sync();
+          take.release(ctl);
+          continue;
+        }
+        m = y.x;
+        l = y.y;
+        if (!PAIR) {
+          f0 = 1.f;
+          has0 = true;
+          has1 = false;
+        }
+      }
+      const bool split = w.parts > 1;
+      float *part =
+          p.part + static_cast<size_t>(w.slot + (w.z & (kMore - 1))) * (C::kRows * (D + 2));
       const int row = (PAIR ? s * kQ : 0) + qr;
       const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;
       f0 *= inv;
@@ -1242,17 +1350,23 @@ size_t sem_bytes(int max_parts) {
   return (256 + static_cast<size_t>(max_parts) * 4 + 255) / 256 * 256;
 }
 
+// Query rows of a CTA, at most, in the forms that such calls take.
+size_t part_rows(int B, int G, int N) {
+  const long long each = (static_cast<long long>(N) * G + B - 1) / B;
+  return each > kQ ? 2 * kQ : each > 32 || G > 32 ? kQ : 32;
+}
+
 }  // namespace
 
 // workspace: [0] items handed out, [1] CTAs ended, from byte 256 the parts' semaphores (all zero
 // between calls), then the parts, as large as any form of these rows needs (so that fewer tokens
-// never need more)
-size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int N, int num_sms) {
+// never need more), and where rows may be longer than a segment the CTAs' sums over segments
+size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int N, int num_sms) {
   const int max_parts = kPartsPerSm * num_sms;
-  const int G = Hq / Hkv;
-  const long long each = (static_cast<long long>(N) * G + B - 1) / B;
-  const size_t rows = each > kQ ? 2 * kQ : each > 32 || G > 32 ? kQ : 32;
-  return sem_bytes(max_parts) + static_cast<size_t>(max_parts) * rows * (D + 2) * 4;
+  const size_t rows = part_rows(B, Hq / Hkv, N);
+  return sem_bytes(max_parts) + static_cast<size_t>(max_parts) * rows * (D + 2) * 4 +
+         (T > kSegment * kKeys ? num_sms * carry_floats(max(static_cast<int>(rows), kQ), D) * 4
+                               : 0);
 }
 
 cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStream_t stream) {
@@ -1263,6 +1377,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStr
   p.done = p.next + 1;
   p.sem = p.next + 64;
   p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + sem_bytes(p.max_parts));
+  p.carry = p.part + p.max_parts * part_rows(a.B, a.Hq / a.Hkv, a.N) * (a.D + 2);
   const Mode mode = choose_mode(a.B, a.Hq, a.Hkv, a.D, a.T, a.N, num_sms);
   p.group = a.Hq / a.Hkv;
   p.tq = (mode == kFew ? 32 : kQ) / p.group;

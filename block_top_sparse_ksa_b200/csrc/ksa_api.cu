@@ -1099,7 +1099,8 @@ ksa_status chunk_common(const ksa_shape *shape, int32_t num_tokens, const uint16
                 "q_stride must be a multiple of 8 elements that holds the token's heads");
   const int sms = device_sm_count();
   const size_t need = ksa::chunk_attn_workspace_bytes(
-      shape->batch, shape->num_q_heads, shape->num_kv_heads, shape->head_dim, num_tokens, sms);
+      shape->batch, shape->num_q_heads, shape->num_kv_heads, shape->head_dim, shape->capacity,
+      num_tokens, sms);
   if (ws == nullptr || ws_bytes < need || !aligned(ws, 256))
     return fail(KSA_ERR_WORKSPACE, "workspace: %zu bytes, 256-byte aligned, are needed (%zu given)",
                 need, ws == nullptr ? static_cast<size_t>(0) : ws_bytes);
@@ -1130,7 +1131,8 @@ ksa_status chunk_common(const ksa_shape *shape, int32_t num_tokens, const uint16
 size_t ksa_chunk_attn_workspace(const ksa_shape *shape, int32_t num_tokens) {
   if (check_chunk(shape, false, num_tokens) != KSA_OK) return 0;
   return ksa::chunk_attn_workspace_bytes(shape->batch, shape->num_q_heads, shape->num_kv_heads,
-                                         shape->head_dim, num_tokens, device_sm_count());
+                                         shape->head_dim, shape->capacity, num_tokens,
+                                         device_sm_count());
 }
 
 ksa_status ksa_chunk_attn(const ksa_shape *shape, int32_t num_tokens, const uint16_t *q,

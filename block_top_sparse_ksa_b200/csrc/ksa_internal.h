@@ -181,7 +181,7 @@ struct ChunkArgs {
   float scale;
   KvLayout kv;
 };
-size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int N, int num_sms);
+size_t chunk_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int N, int num_sms);
 cudaError_t launch_chunk_attn(const ChunkArgs &a, void *ws, int num_sms, cudaStream_t stream);
 
 // Resident CTAs per SM of `func` launched with `threads` threads and `smem`

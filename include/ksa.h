@@ -532,9 +532,10 @@ ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens
  * (NaN, infinities) does not matter.  A query that sees a NaN or infinite score
  * gets NaN; a NaN or infinity in V of a chunk's token may also reach the
  * chunk's earlier queries (a weight of 0 times it).  Scores, the running
- * maximum and sum and the output accumulate in fp32; the weights are rounded to
- * bf16 for the product with V (relative error up to 2^-8 each), and out once to
- * bf16.
+ * maximum and sum and the output accumulate in fp32 (the output over at most
+ * 65536 tokens in the tensor cores, which truncate: up to 3e-4 of it; longer
+ * sums are added up with rounding); the weights are rounded to bf16 for the
+ * product with V (relative error up to 2^-8 each), and out once to bf16.
  *   q:    bf16, token stride q_stride elements (a multiple of 8), heads and
  *         dims dense;  cu_q: [B+1] int32, ascending;  seq_lens: [B] int32
  *         (0 is allowed; outside [0, T] is clamped and flagged)

@@ -1014,3 +1014,56 @@ def test_chunk_attn_tiles_with_idle_warps(ksa, D, n):
     check_attn(ksa, [(n, 2300), (n, 1290), (n, 129)], 8, 2, D, 16, True, True, seed=n)
     check_attn(ksa, [(n, 20011)], 3, 1, D, 32, False, False, seed=n + 1)
     check_attn(ksa, [(n, 2176)] * 40, 24, 8, D, 64, True, False, seed=n + 2)
+
+
+LONG = [  # B, n, G, D, P pages of 64, L (P * 64 tokens over and over), causal
+    (1, 148 * 256, 1, 128, 64, (1 << 20) + 77, False),   # query tiles in pairs, 16 segments and more
+    (1, 148 * 256, 1, 128, 64, 65536, False),            # a whole segment, no second one
+    (1, 148 * 256, 1, 128, 64, 65537, True),             # one token more
+    (1, 148 * 128, 1, 64, 64, 1 << 22, False),           # one tile by one, 64 segments
+    (1, 148 * 20, 5, 64, 3, 200003, True),
+    (40, 700, 1, 128, 3, 90000, True),
+    (148, 1, 8, 128, 64, (1 << 20) + 5, False),          # few rows, whole items
+    (296, 2, 2, 64, 5, 300001, True),
+    (10, 1, 1, 128, 64, 1 << 23, False),                 # cut, the parts in segments
+    (9, 100, 1, 64, 64, 1 << 23, False),
+]
+
+
+@pytest.mark.parametrize("B,n,G,D,P,L,causal", LONG)
+def test_chunk_attn_long_sums(ksa, B, n, G, D, P, L, causal):
+    """Values with a mean over long rows: no drift with the length.  The rows read the same P pages
+    over and over, so that the sums are those over P * 64 tokens, each as often as it is seen.  The
+    bounds are those of short rows.  The mean error: over 512 tiles the tensor cores truncate up to
+    2.6e-4 of a sum; roundings have no direction, their mean over a row's dims is below 1e-4 (bf16
+    weights of 192 tokens or more, 2^-8 / sqrt(12 * 192)), and twice that is allowed.  lse: 512
+    additions of a tile's sum and fewer of segments and parts, 2^-24 each."""
+    bs, pool = 64, P * 64
+    g = torch.Generator(device=DEV)
+    g.manual_seed(L % 1000 + D)
+    K, V = ((torch.randn((P, 1, bs, D), generator=g, device=DEV) + mean).to(torch.bfloat16)
+            for mean in (0.0, 1.0))
+    q = torch.randn((B * n, G, D), generator=g, device=DEV).to(torch.bfloat16)
+    blocks = -(-L // bs)
+    table = (torch.arange(blocks, device=DEV) % P).int()[None].repeat(B, 1)
+    lse, st = torch.empty((B * n, G), device=DEV), status()
+    mask = ksa.MASK_CAUSAL if causal else ksa.MASK_NONE
+    out, _ = ksa.ksa_chunk_attn_paged(q, K, V, table, i32(range(0, B * n + 1, n)), i32([L] * B),
+                                      mask, lse=lse, dev_status=st)
+    assert int(st) == 0
+    k, v = K[:, 0].reshape(pool, D).double(), V[:, 0].reshape(pool, D).double()
+    at = torch.arange(pool, device=DEV)
+    for b in {0, B // 2, B - 1}:
+        for i in {0, n // 2, max(0, n - 129)}:
+            rows = torch.arange(i, min(n, i + 129), device=DEV)
+            seen = L - n + rows + 1 if causal else torch.full_like(rows, L)
+            times = (seen // pool)[:, None] + (at < (seen % pool)[:, None])
+            z = torch.einsum("nhd,td->nht", q[b * n + rows].double(), k) * D ** -0.5
+            z = z + times.double().log()[:, None]
+            want_lse = torch.logsumexp(z, -1)
+            w = torch.exp(z - want_lse[..., None])
+            want, mag = w @ v, w @ v.abs()
+            off = (out[b * n + rows].double() - want).abs()
+            assert bool((off <= (HALF + 4e-4) * mag + HALF * want.abs()).all())
+            assert float(((out[b * n + rows].double() - want) / mag).mean().abs()) <= 5e-4
+            assert float((lse[b * n + rows].double() - want_lse).abs().max()) <= 1e-4
