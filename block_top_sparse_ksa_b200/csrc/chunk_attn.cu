@@ -22,7 +22,9 @@
 //          weighs only the keys [32 w, 32 w + 32) of a key tile (the other
 //          weights of its copy are 0), so the four copies' outputs add up to the
 //          rows' and the softmax of a tile takes a fourth of the time.  With few
-//          rows the call is bound by reading K and V, and only then.
+//          rows the call is bound by reading K and V, and only then.  A weight of
+//          0 times an infinity is NaN, in the three copies that should not weigh
+//          it: where an output is NaN, V is looked through (settle).
 // Two warps load keys and values (TMA; a page's rows of one kv-head are one
 // box), one issues the products, one hands out the work.
 //
@@ -98,10 +100,11 @@ struct Work {
   int len;           // L of the row
   int t0, nt;        // key tiles of this part
   int parts, slot, z;  // parts of the item, the first part's place in the workspace, this part
-                       // (with kBegun: segments of it come before this one; kMore: behind it)
+                       // (and as multiples of kSegments the segments of it before this one, with
+                       // kMore if others are behind it)
 };
 
-constexpr int kBegun = 1 << 30, kMore = 1 << 29;  // see Work::z (below 2^29)
+constexpr int kSegments = 1 << 12, kMore = 1 << 29;  // see Work::z
 
 struct Ctl {  // in shared memory
   uint64_t q_full, q_empty, k_full[8], k_empty[8], v_full[8], v_empty[8];
@@ -111,7 +114,8 @@ struct Ctl {  // in shared memory
   uint64_t work_full[kWork], work_empty[kWork], soft, drain;
   Work work[kWork];
   uint32_t tmem;
-  int abort, last;
+  int abort, alive;  // a wait gave up; when a warp that may work for longer than a wait last did
+  int last;
   uint32_t bad[kBadRing];
   float2 ml[2][kQ];  // m and l of the streams' rows, for their join
 };
@@ -127,14 +131,22 @@ struct Params {
   bool wide_out;          // out is 32-byte aligned
 };
 
-// Waits with a limit; false (and the CTA's abort mark) when it runs out.
+// Time in units of 2^20 ns, as the word behind the abort mark holds it (Ctl::alive).
+__device__ __forceinline__ uint32_t milliseconds() {
+  return static_cast<uint32_t>(global_timer_ns() >> 20);
+}
+
+// Waits with a limit, which a warp at work puts off by Ctl::alive; false (and the CTA's abort mark)
+// when it runs out.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int *abort) {
   if (mbar_try_wait(bar, parity)) return true;
+  volatile int *const word = abort;
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity)) {
-    if (*reinterpret_cast<volatile int *>(abort) != 0) return false;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
-      *reinterpret_cast<volatile int *>(abort) = 1;
+    if (word[0] != 0) return false;
+    if (global_timer_ns() - t0 > kWaitTimeoutNs &&
+        milliseconds() - static_cast<uint32_t>(word[1]) > (kWaitTimeoutNs >> 20)) {
+      word[0] = 1;
       return false;
     }
   }
@@ -420,7 +432,7 @@ __device__ __forceinline__ void hand_out_work(const Params &p, Ctl &ctl, int TT,
     const int all = w.nt, z = w.z;
     for (int done = 0; use; done += kSegment) {
       w.nt = min(all - done, kSegment);
-      w.z = z | (done > 0 ? kBegun : 0) | (all - done > kSegment ? kMore : 0);
+      w.z = z + done / kSegment * kSegments + (all - done > kSegment ? kMore : 0);
       if (!warp_wait(&ctl.work_empty[at], turn, &ctl.abort)) return;
       if (lane == 0) {
         ctl.work[at] = w;
@@ -471,8 +483,67 @@ __host__ __device__ constexpr size_t carry_floats(int rows, int D) {
   return 2 * kSoftWarps * 32 + static_cast<size_t>(rows) * D;
 }
 
+// Outputs of few rows that are not finite.  V is looked through: where a row's keys [first, end)
+// hold infinities of one sign in a dim, and no NaN, that is the sum (finite keys add nothing to
+// it); a row that sees nothing gets 0; all else stays as it is.  By a whole warp, whose rows share
+// b and g and end within a tile's tokens of each other; `mine`: the lane has a row, with no NaN
+// score.  Its outputs, `dims` from `dim` on: bf16 at `out` or, of a part, quads of fp32 `pitch`
+// apart.
+template <int D>
+__device__ __noinline__ void settle(const ChunkArgs &a, Ctl &ctl, const Work &w, int first, int end,
+                                    int dim, int dims, bool mine, uint16_t *out, float4 *part,
+                                    int pitch) {
+  uint32_t nan = 0u, pos = 0u, neg = 0u;  // a bit for each dim
+  const int lane = threadIdx.x & 31;
+  const auto look = [&](int t) {
+    const long long at = kv_row(a.kv, w.b, w.g, a.Hkv, a.T, t);
+    if (at < 0) return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(a.V + at * D + dim);
+    for (int i = 0; i < dims / 8; ++i) {
+      const uint4 x = src[i];
+      const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t h = y[e / 2] >> (16 * (e % 2)) & 0xffffu, bit = 1u << (8 * i + e);
+        if ((h & 0x7f80u) != 0x7f80u) continue;
+        if ((h & 0x7fu) != 0u)
+          nan |= bit;
+        else if (h >> 15)
+          neg |= bit;
+        else
+          pos |= bit;
+      }
+    }
+  };
+  // the keys that all rows see (but those that see none) by all lanes, the others by the lanes
+  // whose rows see them
+  const int all = __reduce_min_sync(0xffffffffu, end > first ? end : INT32_MAX);
+  if (all != INT32_MAX) {
+    for (int t = first + lane, n = 1; t < all; t += 32, ++n) {
+      look(t);
+      if ((n & 4095) == 0)
+        *const_cast<volatile int *>(&ctl.alive) = static_cast<int>(milliseconds());
+    }
+    nan = __reduce_or_sync(0xffffffffu, nan);
+    pos = __reduce_or_sync(0xffffffffu, pos);
+    neg = __reduce_or_sync(0xffffffffu, neg);
+    for (int t = all; t < end; ++t) look(t);
+  }
+  if (!mine) return;
+  const bool nothing = end <= first;
+  for (int e = 0; e < dims; ++e) {
+    const bool p = pos >> e & 1u, n = neg >> e & 1u;
+    if (!nothing && (p == n || (nan >> e & 1u))) continue;
+    const float x = nothing ? 0.f : p ? INFINITY : -INFINITY;
+    if (out != nullptr)
+      out[e] = static_cast<uint16_t>(__float_as_uint(x) >> 16);
+    else
+      reinterpret_cast<float *>(part + e / 4 * pitch)[e % 4] = x;
+  }
+}
+
 // A segment that is not a part's only one, by a softmax warp: the segments before and O of the
-// streams (the warp's own and, but for pairs, the other one; with the weights f0 and f1, 0: none)
+// streams (the warp's own and, but for pairs, the other one; weights f0 and f1, below 0: none)
 // go together.  If more segments follow, the sum goes to the workspace, else over the warp's own
 // O.  Returns its (m, l).
 template <int D, Mode MODE>
@@ -488,13 +559,16 @@ __device__ __forceinline__ float2 add_segment(const Params &p, const Ctl &ctl, c
   float2 *stats = reinterpret_cast<float2 *>(carry) + threadIdx.x;
   float4 *sums = reinterpret_cast<float4 *>(carry + 2 * kSoftWarps * 32) +
                  warp * (DIMS / 4 * 32) + lane;  // [warps][DIMS / 4][32]
-  float f = 0.f;  // of the segments before
-  if (w.z & kBegun) {
+  const bool take0 = !(f0 < 0.f), take1 = !(f1 < 0.f);
+  bool take = false;  // the segments before
+  float f = 0.f;
+  if ((w.z & (kMore - 1)) >= kSegments) {
     const float2 y = *stats;
     const float up = fmaxf(ml.x, y.x);
+    take = y.x != -INFINITY;
     const float g = ml.x == -INFINITY ? 1.f : fast_exp2((ml.x - up) * c);
-    f = y.x == -INFINITY ? 0.f : fast_exp2((y.x - up) * c);
-    ml = make_float2(up, ml.y * g + (y.x == -INFINITY ? y.y : y.y * f));
+    f = take ? fast_exp2((y.x - up) * c) : 0.f;
+    ml = make_float2(up, ml.y * g + (take ? y.y * f : y.y));
     f0 *= g;
     f1 *= g;
   }
@@ -505,21 +579,21 @@ __device__ __forceinline__ float2 add_segment(const Params &p, const Ctl &ctl, c
     float o[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = 0.f;
-    if (__any_sync(0xffffffffu, f0 != 0.f)) {
+    if (__any_sync(0xffffffffu, take0)) {
       tmem_load16(own + i, v);
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        if (f0 != 0.f) o[e] = __uint_as_float(v[e]) * f0;
+        if (take0) o[e] = __uint_as_float(v[e]) * f0;
     }
-    if (__any_sync(0xffffffffu, f1 != 0.f)) {
+    if (__any_sync(0xffffffffu, take1)) {
       tmem_load16(other + i, v);
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        if (f1 != 0.f) o[e] += __uint_as_float(v[e]) * f1;
+        if (take1) o[e] += __uint_as_float(v[e]) * f1;
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (f != 0.f) {
+      if (take) {
         const float4 x = sums[(i / 4 + q) * 32];
         o[4 * q] += x.x * f;
         o[4 * q + 1] += x.y * f;
@@ -636,8 +710,8 @@ __device__ __noinline__ void join_outputs(const Params &p, const Work &w, const 
       for (int q = 0; q < kParts; ++q) {
 #pragma unroll
         for (int i = 0; i < kQuads; ++i) {
-          const bool none = q0 + q >= parts || m[q][i] == -INFINITY;
-          const float f = none ? 0.f : fast_exp2((m[q][i] - st[i].x) * c) * st[i].y;
+          if (q0 + q >= parts || m[q][i] == -INFINITY) continue;  // it may hold NaN
+          const float f = fast_exp2((m[q][i] - st[i].x) * c) * st[i].y;
           o[i].x += x[q][i].x * f;
           o[i].y += x[q][i].y * f;
           o[i].z += x[q][i].z * f;
@@ -700,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.q_empty, 1);
       mbar_init(&ctl.soft, kSoftWarps);
       mbar_init(&ctl.drain, 1);
-      ctl.abort = 0;
+      ctl.abort = ctl.alive = 0;
     }
     fence_mbar_init();
   } else if (warp == kMmaWarp) {
@@ -1101,6 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = qr < G * TQ && tok < w.tokens;
       const long long at = (static_cast<long long>(w.token) + tok) * a.Hq + h;
       float f0 = 1.f, f1 = 0.f;
+      float own = m, other = -INFINITY;  // maxima that the streams' outputs belong to
       bool has0 = steps > 0, has1 = false;
       // every step's product arrives on o_done: the last one's parity is behind `turn`
       if (steps > 0) ok = warp_wait(&ctl.o_done[s], turn ^ 1u, &ctl.abort);
@@ -1112,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (FEW) {  // the row's eight maxima and sums
-        const float own = m, other = ctl.ml[s ^ 1][r].x;
+        other = ctl.ml[s ^ 1][r].x;
         m = -INFINITY;
         l = 0.f;
 #pragma unroll
@@ -1128,6 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (!PAIR) {
         const float2 y = ctl.ml[s ^ 1][r];
         has1 = w.nt > (s ^ 1);
+        other = y.x;
         const float both = fmaxf(m, y.x);
         f0 = m == -INFINITY ? 0.f : fast_exp2((m - both) * c);
         f1 = y.x == -INFINITY ? 0.f : fast_exp2((y.x - both) * c);
@@ -1137,16 +1213,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_fence_after();
       constexpr int kDims = PAIR ? D : D / 2;  // of this warp
       const int dim0 = PAIR ? 0 : s * kDims;
-      if (w.z >= kMore) {
-        const float2 y =
-            add_segment<D, MODE>(p, ctl, w, has0 ? f0 : 0.f, has1 ? f1 : 0.f, make_float2(m, l));
+      if (w.z >= kSegments) {
+        const float2 y = add_segment<D, MODE>(p, ctl, w,
+                                              has0 && own != -INFINITY ? f0 : -1.f,
+                                              has1 && other != -INFINITY ? f1 : -1.f,
+                                              make_float2(m, l));
         if (w.z & kMore) {
           tmem_fence_before();
           if (!PAIR) soft_sync();
           take.release(ctl);
           continue;
         }
-        m = y.x;
+        own = m = y.x;
         l = y.y;
         if (!PAIR) {
           f0 = 1.f;
@@ -1156,11 +1234,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool split = w.parts > 1;
       float *part =
-          p.part + static_cast<size_t>(w.slot + (w.z & (kMore - 1))) * (C::kRows * (D + 2));
+          p.part + static_cast<size_t>(w.slot + (w.z & (kSegments - 1))) * (C::kRows * (D + 2));
       const int row = (PAIR ? s * kQ : 0) + qr;
       const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;
       f0 *= inv;
       f1 *= inv;
+      // A row that sees none of a stream's keys takes nothing of its output, which may be NaN by
+      // values that other rows see.  (Where a score was NaN, so is l, and no weight is 0.)
+      const bool take0 = FEW || own != -INFINITY || f0 != 0.f,
+                 take1 = FEW || other != -INFINITY || f1 != 0.f;
       if (valid && (FEW ? warp == 0 : dim0 == 0)) {
         if (split)
           reinterpret_cast<float2 *>(part)[row] = make_float2(m, l);
@@ -1181,12 +1263,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (has0) {
             tmem_load16(to + dim0 + i, v);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[i + e] = __uint_as_float(v[e]) * f0;
+            for (int e = 0; e < 16; ++e)
+              if (take0) o[i + e] = __uint_as_float(v[e]) * f0;
           }
           if (has1) {
             tmem_load16(tmem + lanes + 2 * kKeys + (s ^ 1) * D + dim0 + i, v);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[i + e] += __uint_as_float(v[e]) * f1;
+            for (int e = 0; e < 16; ++e)
+              if (take1) o[i + e] += __uint_as_float(v[e]) * f1;
           }
         }
         float *sum = sums + ((copy & 1) * 2 + s) * (2 * kOut * 32) + lane;  // [2][2][D / 2][32]
@@ -1202,25 +1286,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         soft_sync();
         if (!ok) break;
-        if (copy < 2 && valid) {
+        if (copy < 2) {
           const float *from = sums + ((copy ^ 1) * 2 + s) * (2 * kOut * 32) + lane;
           const int dim = dim0 + copy * kOut;
 #pragma unroll
           for (int e = 0; e < kOut; ++e) o[e] = (copy == 0 ? o[e] : o[kOut + e]) + from[e * 32];
-          if (split) {
-            float4 *dst =
-                reinterpret_cast<float4 *>(part + 2 * C::kRows) + dim / 4 * C::kRows + row;
+          float4 *dst =
+              split ? reinterpret_cast<float4 *>(part + 2 * C::kRows) + dim / 4 * C::kRows + row
+                    : nullptr;
+          uint16_t *to = split ? nullptr : a.out + at * D + dim;
+          if (valid && split) {
 #pragma unroll
             for (int e = 0; e < kOut / 4; ++e)
               dst[e * C::kRows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else {
-            uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + dim);
+          } else if (valid) {
 #pragma unroll
             for (int e = 0; e < kOut / 8; ++e)
-              dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]),
-                                  pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                  pack_bf16x2(o[8 * e + 4], o[8 * e + 5]),
-                                  pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+              reinterpret_cast<uint4 *>(to)[e] = make_uint4(
+                  pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                  pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+          }
+          float zero[4] = {0.f, 0.f, 0.f, 0.f};  // NaN if an output is not finite
+#pragma unroll
+          for (int e = 0; e < kOut; ++e) zero[e & 3] = fmaf(o[e], 0.f, zero[e & 3]);
+          const bool mine = valid && l == l;
+          if (__any_sync(0xffffffffu,
+                         mine && (zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.f)) {
+            const int keys = w.t0 * kKeys;  // before this segment, and before the part
+            const int first = keys - (w.z & (kMore - 1)) / kSegments * kSegment * kKeys;
+            settle<D>(a, ctl, w, first, keys + min(end, w.nt * kKeys), dim, kOut, mine, to, dst,
+                      C::kRows);
           }
         }
       } else if (active) {
@@ -1233,12 +1328,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (has0) {
             tmem_load32(to + dim0 + i, v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(v[e]) * f0;
+            for (int e = 0; e < 32; ++e)
+              if (take0) o[e] = __uint_as_float(v[e]) * f0;
           }
           if (has1) {
             tmem_load32(tmem + lanes + 2 * kKeys + (s ^ 1) * D + dim0 + i, v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(v[e]) * f1;
+            for (int e = 0; e < 32; ++e)
+              if (take1) o[e] += __uint_as_float(v[e]) * f1;
           }
           if (!valid) continue;
           if (split) {

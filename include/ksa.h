@@ -530,8 +530,10 @@ ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens
  * A query that sees nothing (L_b = 0, or more new tokens than cached ones)
  * gives out = 0 and lse = -inf.  What the cache holds behind a row's L_b tokens
  * (NaN, infinities) does not matter.  A query that sees a NaN or infinite score
- * gets NaN; a NaN or infinity in V of a chunk's token may also reach the
- * chunk's earlier queries (a weight of 0 times it).  Scores, the running
+ * gets NaN.  A NaN or infinity in V of a token that a query sees goes into that
+ * dim of its output as the sum has it (a weight below 2^-126 of the row's
+ * largest counts as 0, and 0 times an infinity is NaN); in V of a chunk's token
+ * it may also reach the chunk's earlier queries, as NaN.  Scores, the running
  * maximum and sum and the output accumulate in fp32 (the output over at most
  * 65536 tokens in the tensor cores, which truncate: up to 3e-4 of it; longer
  * sums are added up with rounding); the weights are rounded to bf16 for the

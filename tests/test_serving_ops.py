@@ -1067,3 +1067,97 @@ def test_chunk_attn_long_sums(ksa, B, n, G, D, P, L, causal):
             assert bool((off <= (HALF + 4e-4) * mag + HALF * want.abs()).all())
             assert float(((out[b * n + rows].double() - want) / mag).mean().abs()) <= 5e-4
             assert float((lse[b * n + rows].double() - want_lse).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,Hq,Hkv,paged,causal", [
+    ([(1, 300), (2, 7), (3, 200), (0, 9)], 4, 2, True, False),      # few rows, whole
+    ([(4, 700), (1, 1), (2, 100), (8, 130)], 4, 2, False, True),
+    ([(1, 40000)], 8, 2, True, False),                              # few rows, cut
+    ([(2, 66000)] * 75, 2, 2, True, True),                          # few rows, in segments
+    ([(100, 300), (60, 140)], 2, 2, True, False),                   # one query tile
+    ([(90, 20000)], 2, 2, False, True),
+    ([(300, 500)] * 20, 16, 8, True, True),                         # pairs
+    ([(300, 9000), (280, 30)], 8, 8, False, False),
+])
+def test_chunk_attn_non_finite_values(ksa, D, rows, Hq, Hkv, paged, causal):
+    """NaN and infinities in V of tokens that every query of the row sees: in every form they add up
+    as the definition has it (weights are above 0), and reach no other dim, row or head."""
+    B, bs = len(rows), 16
+    nq, lens = [r[0] for r in rows], [r[1] for r in rows]
+    near = [L for _, L in rows if L < 60000] or [2000]
+    cache = Cache(near, Hkv, D, bs, paged, seed=D + B)
+    if near != lens:  # long rows read the first pages over and over
+        L0 = 2000
+        table = cache.table[0, :L0 // bs].repeat(B, -(-max(lens) // L0))
+        cache.table = table.contiguous()
+        cache.rows = [tuple(torch.cat([x] * (lens[0] // L0 + 1), 1)[:, :lens[0]]
+                            for x in cache.rows[0])]
+    inf, nan = float("inf"), float("nan")
+    poison = [(0, 3, inf), (1, 5, -inf), (2, 7, nan), (33, 9, inf), (70, 9, inf), (34, 11, inf),
+              (100, 11, -inf), (5, 13, inf), (40, 13, nan), (129, 15, -inf), (6, 33, inf)]
+    for b, (n, L) in enumerate(rows[:len(near)]):
+        free = L - n if causal else L  # seen by all queries
+        for t, d, x in poison:
+            if t < min(free, near[b]):
+                if paged:
+                    cache.V[cache.table[b, t // bs].long(), Hkv - 1, t % bs, d] = x
+                else:
+                    cache.V[b, Hkv - 1, t, d] = x
+                for L1 in range(t, L, 2000 if near != lens else L):
+                    cache.rows[b][1][Hkv - 1, L1, d] = x
+    if near != lens:
+        cache.rows = [cache.rows[0]] * B
+    q = randn((sum(nq), Hq, D), 5)
+    lse, st = torch.empty((sum(nq), Hq), device=DEV), status()
+    out, _ = cache.call(ksa, q, i32(np.concatenate([[0], np.cumsum(nq)])), i32(lens),
+                        ksa.MASK_CAUSAL if causal else ksa.MASK_NONE, lse=lse, dev_status=st)
+    assert int(st) == 0
+    at = 0
+    for b, (n, L) in enumerate(rows):
+        if n and b in (0, 1, 2, 3, B - 1):
+            k, v = cache.rows[b]
+            fine = torch.where(torch.isfinite(v.float()), v.float(), 0.0)
+            want, want_lse, mag = ref_attn(q[at:at + n], k, fine, n, L, causal, D ** -0.5)
+            for x, y in ((inf, inf), (-inf, -inf), (nan, nan)):
+                has = v.isnan().any(1) if x != x else (v == x).any(1)  # [Hkv, D]
+                has = has.repeat_interleave(Hq // Hkv, 0).expand_as(want)
+                if x != x:
+                    want = torch.where(has, nan, want)
+                else:
+                    want = torch.where(has, want + x, want)
+            got = out[at:at + n].double()
+            assert torch.equal(got.isnan(), want.isnan()), b
+            assert torch.equal(got.isinf(), want.isinf())
+            assert torch.equal(got[want.isinf()], want[want.isinf()])
+            ok = torch.isfinite(want)
+            off = (got - want).abs() - (HALF + 4e-4) * mag - HALF * want.abs()
+            assert bool((off[ok] <= 1e-30).all())
+            assert float((lse[at:at + n].double() - want_lse).abs().max()) <= 1e-4
+        at += n
+
+
+@pytest.mark.parametrize("rows,Hq,Hkv", [([(8, 3)], 2, 1), ([(90, 20)], 1, 1),
+                                         ([(300, 200), (300, 40)], 16, 8),
+                                         ([(33, 9)] * 3, 1, 1)])
+def test_chunk_attn_rows_that_see_nothing_beside_infinities(ksa, rows, Hq, Hkv):
+    """More new tokens than cached ones: the first queries see nothing and give 0 and -inf, whatever
+    V holds; queries that see an infinity give it."""
+    D = 64
+    nq, lens = [r[0] for r in rows], [r[1] for r in rows]
+    cache = Cache(lens, Hkv, D, 16, False, 5)
+    cache.V[:, :, 0, 2] = float("inf")
+    cache.V[:, :, 0, 3] = float("nan")
+    q = randn((sum(nq), Hq, D), 6)
+    out, lse = torch.empty_like(q), torch.empty((sum(nq), Hq), device=DEV)
+    cache.call(ksa, q, i32(np.concatenate([[0], np.cumsum(nq)])), i32(lens), ksa.MASK_CAUSAL,
+               out=out, lse=lse)
+    at = 0
+    for n, L in rows:
+        none = n - L
+        assert bool((out[at:at + none] == 0).all())
+        assert bool((lse[at:at + none] == -torch.inf).all())
+        assert bool((out[at + none:at + n, :, 2] == torch.inf).all())
+        assert bool(out[at + none:at + n, :, 3].isnan().all())
+        assert bool(torch.isfinite(out[at + none:at + n, :, 4:].float()).all())
+        at += n
