@@ -1088,7 +1088,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         __uint_as_float(v[i + 1]));
           const float top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]),
                                      max3_nan(mx[6], mx[7], -INFINITY));
-          if (!(top < INFINITY)) l = NAN;  // a NaN or infinite score: so is the row's softmax
+          // a NaN or +inf score: the row's softmax is NaN (-inf weighs nothing)
+          if (!(top < INFINITY)) l = NAN;
           if (APART && k > 0) {  // the last product reads the weights and adds to O
             ok = warp_wait(&ctl.o_done[s], turn, &ctl.abort);
             if (!ok) break;
@@ -1314,8 +1315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                          mine && (zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.f)) {
             const int keys = w.t0 * kKeys;  // before this segment, and before the part
             const int first = keys - (w.z & (kMore - 1)) / kSegments * kSegment * kKeys;
-            settle<D>(a, ctl, w, first, keys + min(end, w.nt * kKeys), dim, kOut, mine, to, dst,
-                      C::kRows);
+            settle<D>(a, ctl, w, first, l == 0.f ? first : keys + min(end, w.nt * kKeys), dim,
+                      kOut, mine, to, dst, C::kRows);
           }
         }
       } else if (active) {

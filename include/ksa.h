@@ -529,11 +529,13 @@ ksa_status ksa_rotary_append_kv_paged(const ksa_shape *shape, int32_t num_tokens
  *   out[n,h,:] = sum_t w_t V[b,g,t,:],  lse[n,h] = log sum_t exp(z_t).
  * A query that sees nothing (L_b = 0, or more new tokens than cached ones)
  * gives out = 0 and lse = -inf.  What the cache holds behind a row's L_b tokens
- * (NaN, infinities) does not matter.  A query that sees a NaN or infinite score
- * gets NaN.  A NaN or infinity in V of a token that a query sees goes into that
- * dim of its output as the sum has it (a weight below 2^-126 of the row's
- * largest counts as 0, and 0 times an infinity is NaN); in V of a chunk's token
- * it may also reach the chunk's earlier queries, as NaN.  Scores, the running
+ * (NaN, infinities) does not matter.  A query that sees a NaN or +inf score gets
+ * NaN, in lse too; a score of -inf weighs nothing, and a query all of whose
+ * scores are -inf gives out = 0 and lse = -inf.  A NaN or infinity in V of a
+ * token that a query sees goes into that dim of its output as the sum has it (an
+ * infinity whose weight is 0, by a score of -inf or below 2^-126 of the largest,
+ * may give NaN); in V of a chunk's token it may also reach the chunk's earlier
+ * queries, as NaN.  Scores, the running
  * maximum and sum and the output accumulate in fp32 (the output over at most
  * 65536 tokens in the tensor cores, which truncate: up to 3e-4 of it; longer
  * sums are added up with rounding); the weights are rounded to bf16 for the

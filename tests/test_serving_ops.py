@@ -1161,3 +1161,40 @@ def test_chunk_attn_rows_that_see_nothing_beside_infinities(ksa, rows, Hq, Hkv):
         assert bool(out[at + none:at + n, :, 3].isnan().all())
         assert bool(torch.isfinite(out[at + none:at + n, :, 4:].float()).all())
         at += n
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows,Hq,Hkv", [
+    ([(2, 200), (1, 50), (3, 129)], 2, 1), ([(1, 30000)], 4, 1), ([(100, 300)], 1, 1),
+    ([(90, 20000)], 1, 1), ([(300, 500)] * 20, 8, 8), ([(300, 9000), (260, 129)], 8, 8)])
+def test_chunk_attn_scores_of_minus_infinity(ksa, D, rows, Hq, Hkv):
+    """A score of -inf weighs nothing; a row of nothing but -inf gives 0 and -inf, also where V holds
+    infinities; +inf gives NaN."""
+    nq, lens = [r[0] for r in rows], [r[1] for r in rows]
+    cache = Cache(lens, Hkv, D, 16, False, 3)
+    q = randn((sum(nq), Hq, D), 7).abs() + 0.5
+    cu, seq = i32(np.concatenate([[0], np.cumsum(nq)])), i32(lens)
+    lse = torch.empty((sum(nq), Hq), device=DEV)
+    for b, L in enumerate(lens):  # every third token only
+        cache.rows[b][0][:] = torch.where(torch.arange(L, device=DEV)[:, None] % 3 == 0,
+                                          cache.rows[b][0].float(), -torch.inf).bfloat16()
+        cache.K[b, :, :L] = cache.rows[b][0]
+    out, _ = cache.call(ksa, q, cu, seq, ksa.MASK_NONE, lse=lse)
+    at = 0
+    for b, (n, L) in enumerate(rows):
+        k, v = (x[:, ::3] for x in cache.rows[b])
+        want, want_lse, mag = ref_attn(q[at:at + n], k, v, n, k.shape[1], False, D ** -0.5)
+        off = (out[at:at + n].double() - want).abs() - (HALF + 4e-4) * mag - HALF * want.abs()
+        assert bool((off <= 1e-30).all())
+        assert float((lse[at:at + n].double() - want_lse).abs().max()) <= 1e-4
+        at += n
+    for x in (-torch.inf, torch.inf):
+        for b, L in enumerate(lens):
+            cache.K[b, :, :L] = -torch.inf
+            cache.K[b, :, L // 2] = x
+            cache.V[b, :, L // 3] = torch.inf
+        out, _ = cache.call(ksa, q, cu, seq, ksa.MASK_NONE, lse=lse)
+        if x < 0:
+            assert bool((out == 0).all()) and bool((lse == -torch.inf).all())
+        else:
+            assert bool(out.isnan().all()) and bool(lse.isnan().all())
