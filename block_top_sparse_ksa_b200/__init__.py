@@ -17,16 +17,14 @@ Layouts (row-major, contiguous):
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
+import sys
+import warnings
 from typing import Optional
 
 import numpy as np
 import torch
-
-try:
-    from . import _marshal  # built beside libksa.so; without it every call goes the long way
-except ImportError:
-    _marshal = None
 
 __all__ = [
     "KsaError", "Shape", "lib", "library_path", "ksa_build_block_summaries",
@@ -158,15 +156,37 @@ _SIGS = {
 }
 
 _LIB: Optional[ctypes.CDLL] = None
+# the serving calls' short way, built beside libksa.so and loaded with it; without it every call
+# goes the long way
+_marshal = None
 # addresses of the entry points that _marshal calls, once the library is loaded
 _SHORT = ("ksa_assign_pages", "ksa_release_pages", "ksa_rotary_append_kv",
           "ksa_rotary_append_kv_paged", "ksa_chunk_attn", "ksa_chunk_attn_paged")
 _ENTRIES: dict = {}
 
 
+def _built_for() -> str:
+    """What _marshal.so is compiled against: it reads tensors by torch's binary layout."""
+    return f"torch {torch.__version__} python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def _load_marshal():
+    """_marshal.so, or None where it is missing or built for another torch or Python."""
+    try:
+        short = importlib.import_module("._marshal", __name__)
+    except ImportError:
+        return None
+    built = getattr(short, "built_for", "an unknown torch")
+    if built != _built_for():
+        warnings.warn(f"_marshal.so is built for {built}, not {_built_for()}, and not used; rebuild "
+                      "it with: python -m block_top_sparse_ksa_b200.build")
+        return None
+    return short
+
+
 def lib() -> ctypes.CDLL:
     """The loaded libksa (raises if it was never built)."""
-    global _LIB
+    global _LIB, _marshal
     if _LIB is None:
         if not os.path.exists(library_path):
             raise RuntimeError(
@@ -177,6 +197,7 @@ def lib() -> ctypes.CDLL:
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
+        _marshal = _load_marshal()
         if _marshal is not None:
             for name in _SHORT:
                 _ENTRIES[name] = ctypes.cast(getattr(handle, name), ctypes.c_void_p).value

@@ -1,5 +1,6 @@
 """Build libksa.so (the CUDA library behind include/ksa.h) in-tree for sm_100a, and _marshal.so
-(the Python binding's short way to its serving calls, against the installed torch).
+(the Python binding's short way to its serving calls, against the installed torch; the binding
+does without where it cannot be built).
 
 Usage: ``python -m block_top_sparse_ksa_b200.build [--force] [--verbose]``.
 nvcc cross-compiles without a GPU; the result sits next to this file so it
@@ -13,6 +14,8 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+
+from . import _built_for as built_for
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -41,11 +44,25 @@ def _inputs():
             glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__])
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
+def _newer_than_inputs(path: str) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path)
+                                        for p in _inputs())
+
+
+def _marshal_up_to_date() -> bool:
+    if not _newer_than_inputs(MARSHAL):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    with open(MARSHAL, "rb") as f:  # it reads tensors by the layout of the torch it was built for
+        return built_for().encode() in f.read()
+
+
+def up_to_date() -> bool:
+    return _newer_than_inputs(LIB) and os.path.exists(REPORT) and _marshal_up_to_date()
+
+
+def _lib_command():
+    return [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xptxas=-v", "-Xcompiler", "-fPIC",
+            "-shared", "-o", LIB + ".tmp", *sources()]
 
 
 def _marshal_command():
@@ -56,32 +73,52 @@ def _marshal_command():
                sysconfig.get_paths()["include"]]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            f'-DKSA_BUILT_FOR="{built_for()}"',
             *(f"-I{i}" for i in include), os.path.join(HERE, "csrc", "marshal.cpp"),
             "-o", MARSHAL + ".tmp", f"-L{os.path.join(at, 'lib')}", "-ltorch_python",
             "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _start_marshal():
+    """The compiler of _marshal.so, or None and what went wrong."""
+    try:
+        return subprocess.Popen(_marshal_command(), stdout=subprocess.PIPE,
+                                stderr=subprocess.STDOUT, text=True), ""
+    except Exception as e:  # no g++, no torch headers: the binding does without
+        return None, f"{type(e).__name__}: {e}\n"
+
+
+def _finish_marshal(beside, said: str) -> None:
+    if beside is not None:
+        said = beside.communicate()[0]
+        if beside.returncode == 0:
+            os.replace(MARSHAL + ".tmp", MARSHAL)
+            return
+    if os.path.exists(MARSHAL):  # of other sources, or another torch
+        os.remove(MARSHAL)
+    sys.stderr.write(said + "_marshal.so could not be built; the binding's serving calls check "
+                            "their arguments in Python instead (6 us a call more)\n")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date() and os.path.exists(REPORT):
-        return LIB
-    cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xptxas=-v", "-Xcompiler", "-fPIC",
-           "-shared", "-o", LIB + ".tmp", *sources()]
-    marshal = _marshal_command()
-    beside = subprocess.Popen(marshal, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    said = beside.communicate()[0]
-    for code, what, text in ((res.returncode, cmd, res.stdout + res.stderr),
-                             (beside.returncode, marshal, said)):
-        if code != 0:
-            sys.stderr.write(text)
-            raise subprocess.CalledProcessError(code, what)
-    if verbose:
-        sys.stderr.write(res.stderr)
-    os.makedirs(os.path.dirname(REPORT), exist_ok=True)
-    with open(REPORT, "w") as f:
-        f.write(res.stderr)
-    os.replace(MARSHAL + ".tmp", MARSHAL)
-    os.replace(LIB + ".tmp", LIB)
+    lib = force or not _newer_than_inputs(LIB) or not os.path.exists(REPORT)
+    beside = _start_marshal() if force or not _marshal_up_to_date() else None
+    try:
+        if lib:
+            cmd = _lib_command()
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            if res.returncode != 0:
+                sys.stderr.write(res.stdout + res.stderr)
+                raise subprocess.CalledProcessError(res.returncode, cmd)
+            if verbose:
+                sys.stderr.write(res.stderr)
+            os.makedirs(os.path.dirname(REPORT), exist_ok=True)
+            with open(REPORT, "w") as f:
+                f.write(res.stderr)
+            os.replace(LIB + ".tmp", LIB)
+    finally:
+        if beside is not None:
+            _finish_marshal(*beside)
     return LIB
 
 

@@ -288,4 +288,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal(void) {
+  PyObject *m = PyModule_Create(&module);
+  // the torch and Python whose layouts are compiled in: the binding uses no other build
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", KSA_BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -590,3 +590,40 @@ def test_chunk_attention_waits_end_for_whole_warps():
     loops = re.findall(r"(?:for|while) \([^\n]*\bok\b[^\n]*", products)
     assert loops == ["while (ok && take.get(ctl, w) && w.token >= 0) {"]
     assert re.search(r"ok = __all_sync\(0xffffffffu, ok\);\s*}\s*mma_commit", products)
+
+
+def test_library_is_built_where_the_short_way_cannot_be(ksa, tmp_path, monkeypatch, capsys):
+    """A compiler that is missing or fails leaves libksa.so built and no stale _marshal.so."""
+    import shutil
+    from block_top_sparse_ksa_b200 import build
+    real = build.LIB
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libksa.so"))
+    monkeypatch.setattr(build, "MARSHAL", str(tmp_path / "_marshal.so"))
+    monkeypatch.setattr(build, "REPORT", str(tmp_path / "_build" / "ptxas.txt"))
+    monkeypatch.setattr(build, "_lib_command", lambda: ["cp", real, build.LIB + ".tmp"])
+    for command in (["false"], [str(tmp_path / "no_such_compiler")]):
+        monkeypatch.setattr(build, "_marshal_command", lambda: command)
+        (tmp_path / "_marshal.so").write_bytes(b"of other sources")
+        assert build.build(force=True) == build.LIB
+        assert os.path.exists(build.LIB) and os.path.exists(build.REPORT)
+        assert not os.path.exists(build.MARSHAL) and not build.up_to_date()
+        assert "_marshal.so could not be built" in capsys.readouterr().err
+        os.remove(build.LIB)
+    # and a library that fails to build is still an error, the marshal built or not
+    monkeypatch.setattr(build, "_lib_command", lambda: ["false"])
+    with pytest.raises(Exception, match="false"):
+        build.build(force=True)
+
+
+def test_short_way_of_another_torch_is_not_used(ksa, monkeypatch):
+    """_marshal.so reads tensors by the layout of the torch it was compiled against: after torch is
+    exchanged it counts as out of date, and is not used until it is built again."""
+    from block_top_sparse_ksa_b200 import build
+    ksa.lib()
+    assert build.up_to_date() and ksa._load_marshal() is ksa._marshal
+    other = lambda: "torch 9.9.9 python 3.12"
+    monkeypatch.setattr(build, "built_for", other)
+    assert not build.up_to_date()
+    monkeypatch.setattr(ksa, "_built_for", other)
+    with pytest.warns(UserWarning, match="built for torch"):
+        assert ksa._load_marshal() is None
