@@ -326,15 +326,15 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleaseAr
           flag_status(a.status, KSA_FLAG_INDEX_SKIPPED);
           page[i] = -1;
         }
-        const int at = F + (total - 1 - (lo + i * kThreads));
-        if (at < a.num_pages) a.free_pages[at] = page[i];
+        const int above = total - 1 - (lo + i * kThreads);  // the top; F + above may pass 2^31
+        if (above < a.num_pages - F) a.free_pages[F + above] = page[i];
       }
     }
   }
   if (!last_cta(a.counter, &flag)) return;
   for (int b = threadIdx.x; b < a.B; b += kThreads)
     if (a.done[b] != 0) a.seq_lens[b] = 0;
-  if (threadIdx.x == 0) *a.num_free = min(F + total, a.num_pages);
+  if (threadIdx.x == 0) *a.num_free = F + min(total, a.num_pages - F);
 }
 
 }  // namespace

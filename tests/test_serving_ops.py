@@ -253,6 +253,21 @@ def test_release_flags_bad_entries_and_a_full_stack(ksa):
     assert int(st) == (1 | 2 | 16) and bool((table == -1).all()) and seq.tolist() == [0, 0]
 
 
+def test_release_onto_the_largest_stack(ksa):
+    """A full stack of 2^31 - 1 places: what does not fit is dropped, nothing is written before or
+    behind the stack, and the count stays at its size."""
+    bs, pages, room = 16, 2 ** 31 - 1, 3
+    around = torch.full((pages + 64,), -7, dtype=torch.int32, device=DEV)
+    stack = around[32:32 + pages]
+    table = torch.arange(20, dtype=torch.int32, device=DEV).view(2, 10)
+    seq, count, st = i32([160, 155]), i32([pages - room]), status()
+    ksa.ksa_release_pages(seq, i32([1, 1]), table, stack, count, bs, dev_status=st)
+    assert int(st) == 16 and int(count) == pages and seq.tolist() == [0, 0]
+    assert stack[-room:].tolist() == [19, 18, 17] and bool((table == -1).all())
+    stack[-room:] = -7
+    assert all(bool((part == -7).all()) for part in around.chunk(16))
+
+
 # ---------------------------------------------------------------------------
 # rotary
 
