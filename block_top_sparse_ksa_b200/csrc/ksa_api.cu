@@ -1004,8 +1004,7 @@ ksa_status rotary_common(const ksa_shape *shape, int32_t num_tokens, const ksa_r
   a.v_stride = v_stride;
   a.q_out_stride = q_out_stride;
   a.slots_per_page = paged ? shape->block_size : shape->capacity;
-  a.num_slots = !kv ? INT32_MAX
-                    : static_cast<long long>(a.slots_per_page) * (paged ? num_pages : shape->batch);
+  a.num_slots = static_cast<long long>(a.slots_per_page) * (paged && kv ? num_pages : shape->batch);
   a.N = num_tokens;
   a.Hq = shape->num_q_heads;
   a.Hkv = shape->num_kv_heads;

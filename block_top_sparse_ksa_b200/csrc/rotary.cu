@@ -107,12 +107,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         }
       }
       if (tid < nt) {
+        if (a.k == nullptr) my_slot = min(my_slot, 0LL);  // no cache: padding or not
         if (my_slot >= a.num_slots) {
           flag_status(a.status, KSA_FLAG_INDEX_SKIPPED);
           my_slot = -1;
         }
         long long at = -1;
-        if (my_slot >= 0) {  // (a call without a cache comes here with slot 0)
+        if (my_slot >= 0) {
           const int s = static_cast<int>(my_slot), page = s / a.slots_per_page;
           at = (static_cast<long long>(page) * a.Hkv * a.slots_per_page +
                 (s - page * a.slots_per_page)) * D;

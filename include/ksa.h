@@ -485,7 +485,8 @@ typedef struct {
  * slot s = b * T + t in a contiguous cache, s = page * bs + offset in a paged
  * one (the slots of ksa_assign_pages).  A negative slot is padding: nothing of
  * the token is written.  A slot past the cache likewise, and it sets
- * KSA_FLAG_INDEX_SKIPPED.  Slots must be distinct.
+ * KSA_FLAG_INDEX_SKIPPED (without a cache every slot >= 0 is a real token).
+ * Slots must be distinct.
  *   rotary:    read before the call returns; NULL: K/V are written unrotated
  *              (encoder states), q must then be NULL
  *   q, q_out:  bf16, token strides q_stride and q_out_stride elements, heads

@@ -372,6 +372,22 @@ def test_rotary_parts(ksa):
                                     rot).shape == (0, Hq, D)
 
 
+@pytest.mark.parametrize("paged", [True, False])
+def test_rotary_of_queries_with_slots_of_another_cache(ksa, paged):
+    """Queries only: a slot says no more than whether the token is real, however far it is."""
+    N, Hq, D = 9, 4, 64
+    q, pos = randn((N, Hq, D), 4), torch.arange(N, dtype=torch.int32, device=DEV)
+    rot, st = ksa.Rotary([0.3 ** i for i in range(32)]), status()
+    want = ksa.ksa_rotary_append_kv(q, None, None, pos, None, None, None, rot)
+    slots = torch.tensor([0, 5, 2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31, 2 ** 40, 2 ** 62, -1, -2 ** 40],
+                         device=DEV)
+    out = torch.full_like(q, 3.0)
+    call = ksa.ksa_rotary_append_kv_paged if paged else ksa.ksa_rotary_append_kv
+    call(q, None, None, pos, slots, None, None, rot, q_out=out, dev_status=st)
+    assert int(st) == 0
+    assert torch.equal(out[:7], want[:7]) and bool((out[7:] == 3.0).all())
+
+
 def test_rotary_offsets_past_32_bits(ksa):
     """A pool of more than 2^31 elements: the last page's rows land where they belong."""
     Hkv, bs, D = 8, 64, 128
