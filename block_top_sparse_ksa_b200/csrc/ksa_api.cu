@@ -1128,10 +1128,16 @@ ksa_status chunk_common(const ksa_shape *shape, int32_t num_tokens, const uint16
 }  // namespace
 
 size_t ksa_chunk_attn_workspace(const ksa_shape *shape, int32_t num_tokens) {
-  if (check_chunk(shape, false, num_tokens) != KSA_OK) return 0;
-  return ksa::chunk_attn_workspace_bytes(shape->batch, shape->num_q_heads, shape->num_kv_heads,
-                                         shape->head_dim, shape->capacity, num_tokens,
-                                         device_sm_count());
+  size_t bytes = 0;
+  guarded([&]() -> ksa_status {
+    const ksa_status st = check_chunk(shape, false, num_tokens);
+    if (st == KSA_OK)
+      bytes = ksa::chunk_attn_workspace_bytes(shape->batch, shape->num_q_heads,
+                                              shape->num_kv_heads, shape->head_dim,
+                                              shape->capacity, num_tokens, device_sm_count());
+    return st;
+  });
+  return bytes;
 }
 
 ksa_status ksa_chunk_attn(const ksa_shape *shape, int32_t num_tokens, const uint16_t *q,

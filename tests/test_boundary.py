@@ -627,3 +627,21 @@ def test_short_way_of_another_torch_is_not_used(ksa, monkeypatch):
     monkeypatch.setattr(ksa, "_built_for", other)
     with pytest.warns(UserWarning, match="built for torch"):
         assert ksa._load_marshal() is None
+
+
+def test_serving_entries_keep_exceptions_inside():
+    """No exception (out of host memory, for a message) leaves a serving call's C entry: each one's
+    body runs guarded."""
+    path = os.path.join(ROOT, "block_top_sparse_ksa_b200", "csrc", "ksa_api.cu")
+    with open(path) as f:
+        text = f.read()
+    for name in ("ksa_assign_pages", "ksa_release_pages", "ksa_rotary_append_kv",
+                 "ksa_rotary_append_kv_paged", "ksa_chunk_attn_workspace", "ksa_chunk_attn",
+                 "ksa_chunk_attn_paged"):
+        body = re.search(r"^(?:ksa_status|size_t) " + name + r"\([^{]*\{\n(.*?)^}", text,
+                         re.S | re.M).group(1)
+        lines = [x.strip() for x in body.splitlines() if x.strip()]
+        start = next(i for i, x in enumerate(lines) if "guarded([&]() -> ksa_status {" in x)
+        assert all(re.fullmatch(r"size_t \w+ = 0;", x) for x in lines[:start]), name
+        end = lines.index("});")
+        assert lines[end + 1:] in ([], ["return bytes;"]), name
