@@ -1229,3 +1229,86 @@ def test_chunk_attn_scores_of_minus_infinity(ksa, D, rows, Hq, Hkv):
             assert bool((out == 0).all()) and bool((lse == -torch.inf).all())
         else:
             assert bool(out.isnan().all()) and bool(lse.isnan().all())
+
+
+def test_chunk_attn_forms_take_turns_on_one_workspace(ksa):
+    """One workspace, as large as the largest call asks for, for whole, cut and segmented calls of
+    every form at both head sizes: each gives what it gives on a workspace of its own, and leaves
+    the counters and semaphores at zero."""
+    calls = []
+    for D in (128, 64):
+        for rows, Hq, Hkv, T in (([(2, 300), (1, 40)], 8, 2, 0), ([(3, 30000)], 8, 2, 0),
+                                 ([(100, 700), (80, 129)], 2, 2, 0), ([(90, 20000)], 2, 2, 0),
+                                 ([(300, 500)] * 20, 16, 8, 0), ([(300, 9000), (260, 30)], 8, 8, 0),
+                                 ([(2, 66000)] * 75, 2, 2, 2000)):
+            nq, lens = [r[0] for r in rows], [r[1] for r in rows]
+            cache = Cache([T] if T else lens, Hkv, D, 16, True, D)
+            if T:  # the first pages over and over
+                cache.table = cache.table[0, :T // 16].repeat(len(rows), lens[0] // T).contiguous()
+            q = randn((sum(nq), Hq, D), 9)
+            cu, seq = i32(np.concatenate([[0], np.cumsum(nq)])), i32(lens)
+            need = ksa.ksa_chunk_attn_workspace(len(rows), Hq, Hkv, D, cache.table.shape[1] * 16,
+                                                q.shape[0])
+            lse = torch.empty((q.shape[0], Hq), device=DEV)
+            own = torch.zeros(need, dtype=torch.uint8, device=DEV)
+            out, _ = cache.call(ksa, q, cu, seq, ksa.MASK_CAUSAL, lse=lse, workspace=own)
+            calls.append((cache, q, cu, seq, out, lse, need))
+    ws = torch.zeros(max(c[-1] for c in calls), dtype=torch.uint8, device=DEV)
+    marks = 256 + 4 * 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(4)
+    for _ in range(3):
+        for i in rng.permutation(len(calls)):
+            cache, q, cu, seq, out, lse, _ = calls[i]
+            lse2, st = torch.empty_like(lse), status()
+            got, _ = cache.call(ksa, q, cu, seq, ksa.MASK_CAUSAL, lse=lse2, workspace=ws,
+                                dev_status=st)
+            assert torch.equal(got, out) and torch.equal(lse2, lse) and int(st) == 0
+            assert not bool(ws[:marks].any())
+
+
+@pytest.mark.parametrize("rows,tail,Hq,Hkv", [
+    ([(1, 1000 + 37 * b) for b in range(31)] + [(300, 2100)], 0, 8, 2),  # decode rows and a chunk
+    ([(1, 129 * (b + 1)) for b in range(20)] + [(512, 512), (1, 3)], 0, 32, 8),
+    ([(1, 700 + b) for b in range(16)], 500, 8, 2),                      # a padded token axis
+    ([(1, 700 + b) for b in range(16)], 8000, 32, 8),
+    ([(0, 0), (5, 5), (0, 900), (2, 1500)], 100, 16, 2)])
+def test_chunk_attn_mixed_batches_and_padded_axes(ksa, rows, tail, Hq, Hkv):
+    check_attn(ksa, rows, Hq, Hkv, 128, 16, True, True, seed=len(rows) + tail, tail=tail)
+
+
+@pytest.mark.parametrize("N", [8, 90, 2000])
+def test_captured_chunk_attn_follows_the_lengths(ksa, N):
+    """A captured call whose rows change from replay to replay, from all tokens in one row to one
+    token in each, and to none: what an eager call gives."""
+    B, Hq, Hkv, D, bs = 4, 8, 4, 64, 16
+    cache = Cache([3000] * B, Hkv, D, bs, True, 11)
+    q = randn((N, Hq, D), 12)
+    cu, seq, st = i32([0] * (B + 1)), i32([0] * B), status()
+    out, lse = torch.empty_like(q), torch.empty((N, Hq), device=DEV)
+    ws = torch.zeros(ksa.ksa_chunk_attn_workspace(B, Hq, Hkv, D, cache.table.shape[1] * bs, N),
+                     dtype=torch.uint8, device=DEV)
+    call = lambda: cache.call(ksa, q, cu, seq, ksa.MASK_CAUSAL, out=out, lse=lse, workspace=ws,
+                              dev_status=st)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    n = N // 4
+    for nq, lens in (([N, 0, 0, 0], [3000, 5, 0, 7]), ([1, 1, 1, 1], [1, 3000, 128, 129]),
+                     ([0, 0, 0, 0], [9, 9, 9, 9]), ([n, 0, n, 1], [n, 40, 2999, 2]),
+                     ([0, 0, 1, N - 1], [0, 0, 777, 3000])):
+        cu.copy_(i32(np.concatenate([[0], np.cumsum(nq)])))
+        seq.copy_(i32(lens))
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        at = 0
+        for b, (m, L) in enumerate(zip(nq, lens)):
+            k, v = (x[:, :L] for x in cache.rows[b])
+            want, _, mag = ref_attn(q[at:at + m], k, v, m, L, True, D ** -0.5)
+            off = (out[at:at + m].double() - want).abs() - (HALF + 4e-4) * mag - HALF * want.abs()
+            assert bool((off <= 1e-30).all()), (nq, b)
+            at += m
+        assert bool((out[at:] == 5.0).all()) and int(st) == 0
+    del graph
