@@ -10,6 +10,11 @@
 // m only moves when a row's maximum rose by more than a factor 2^8 in weight
 // (P then stays below 2^8 and l and O far inside fp32), so O is rescaled a few
 // times per row and not once per tile; the quotient O / l does not depend on m.
+// l sums the weights in fp32; the product with V takes them rounded to bf16, each
+// off by 2^-8 of itself at most, up or down, so that outputs are off by 0.0020 to
+// 0.0024 (2-norm) where the rounding of outputs alone gives 0.0016.  Two bf16
+// pieces a weight, as the decode attention has them, would make three products of
+// two: half as much again where products bound the call.
 //
 // Layout.  One CTA per SM holds two streams, each with its S and O in tensor
 // memory (2 x (128 + D) of 512 columns; P overwrites the first half of S, or has
@@ -1401,17 +1406,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && ctl.abort != 0) flag_status(a.status, KSA_FLAG_WAIT_TIMEOUT);
 }
 
-// By the rows (tokens times heads of a group) of an average sequence.  What fits in 32 goes as
+// By what the host knows: the rows (tokens times heads of a group) of an average sequence and the
+// capacity T; the lengths are on the device.  Every form serves every length, but a batch far from
+// its average (one-token rows beside a prompt's chunk, an axis that is mostly padding) or far below
+// its capacity is not in the form that would be the fastest for it.  What fits in 32 goes as
 // kFew: one token over 200 to 1500 states (32 sequences, 16 heads of 64) 32 us, 43 as kOne;
 // 5 tokens over 131000 (32 heads on 8 of 128) 96 and 101.  More than a tile of 128 can go in
 // pairs, whose tiles share their keys' loads, or one by one, in items of half the length:
 //   - by the rounds that the SMs take, at 1.2 of a pair's time for two items (6000 keys, 32 heads
 //     on 8 of 128: 512 tokens 73 us in pairs, 55 one by one; 1216: 130 and 122; 1920: 169 and
 //     172; 4800: 381 and 411);
-//   - at D = 64, where the loads are half as large and twice as many places hold them, over more
-//     than 2048 keys always one by one (16384 keys, 2368 tokens: 474 and 437 us; over 1024 keys
-//     39 and 40);
-//   - over one key tile the second stream of a single item has no work, so a round costs the same.
+//   - at D = 64, where the loads are half as large and twice as many places hold them, with room
+//     for more than 2048 keys always one by one (16384 keys, 2368 tokens: 474 and 437 us; over
+//     1024 keys 39 and 40);
+//   - with room for one key tile the second stream of a single item has no work, so a round costs
+//     the same.
 Mode choose_mode(int B, int Hq, int Hkv, int D, int T, int N, int num_sms) {
   const int G = Hq / Hkv;
   const long long rows = static_cast<long long>(N) * G, each = (rows + B - 1) / B;
