@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib
+import operator
 import os
 import sys
 import warnings
@@ -811,6 +812,14 @@ def ksa_select_tokens_one_head(q: torch.Tensor, K: torch.Tensor, seq_lens: torch
 # if that fails.
 
 
+def _int32(v, name: str) -> int:
+    """A whole number that the library takes as 32 bits (ctypes would cut it off silently)."""
+    v = operator.index(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} {v} does not fit in 32 bits")
+    return v
+
+
 def _device_of(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -917,6 +926,8 @@ def ksa_assign_pages(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table
             return ksa_assign_pages(ctx_lens, new_lens, block_table, free_pages, num_free,
                                     block_size, num_tokens, num_free_out, seq_lens, cu_new, slots,
                                     positions, workspace, dev_status)
+    block_size = _int32(block_size, "block_size")
+    num_tokens = _int32(num_tokens, "num_tokens")
     i32 = torch.int32
     B, mb = block_table.shape
     if num_free_out is None:
@@ -963,6 +974,7 @@ def ksa_release_pages(seq_lens: torch.Tensor, done: torch.Tensor, block_table: t
         with _using(stream, dev):
             return ksa_release_pages(seq_lens, done, block_table, free_pages, num_free,
                                      block_size, workspace, dev_status)
+    block_size = _int32(block_size, "block_size")
     i32 = torch.int32
     B, mb = block_table.shape
     pages = free_pages.numel()
@@ -986,11 +998,11 @@ class Rotary:
         as_list = lambda x: x.tolist() if hasattr(x, "tolist") else list(x)
         freq = [float(f) for f in as_list(inv_freq)]
         P = len(freq)
-        self.num_axes = 1 if num_axes is None else int(num_axes)
+        self.num_axes = 1 if num_axes is None else _int32(int(num_axes), "num_axes")
         self._freq = (ctypes.c_double * max(P, 1))(*freq)
         self._axis = None
         if axis_of_pair is not None:
-            axis = [int(i) for i in as_list(axis_of_pair)]
+            axis = [_int32(int(i), "axis_of_pair") for i in as_list(axis_of_pair)]
             if len(axis) != P:
                 raise ValueError(f"axis_of_pair must hold {P} axes, got {len(axis)}")
             self._axis = (ctypes.c_int32 * max(P, 1))(*axis)
@@ -1141,6 +1153,7 @@ def _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse, wor
         with _using(stream, dev):
             return _chunk_attn(q, K, V, block_table, cu_q, seq_lens, mask, scale, out, lse,
                                workspace, dev_status, None)
+    mask = _int32(mask, "mask")
     qs = _token_rows(q, "q", dev)
     N, Hq, D = q.shape
     if not isinstance(K, torch.Tensor) or K.dim() != 4 or K.shape[3] != D:

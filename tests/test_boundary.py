@@ -645,3 +645,10 @@ def test_serving_entries_keep_exceptions_inside():
         assert all(re.fullmatch(r"size_t \w+ = 0;", x) for x in lines[:start]), name
         end = lines.index("});")
         assert lines[end + 1:] in ([], ["return bytes;"]), name
+
+
+def test_rotary_refuses_numbers_past_32_bits(ksa):
+    """An axis or a number of axes past 32 bits is not cut off."""
+    for kw in (dict(num_axes=(1 << 32) + 1), dict(axis_of_pair=[0] * 31 + [1 << 32])):
+        with pytest.raises(ValueError, match="32 bits"):
+            ksa.Rotary([0.5] * 32, **kw)

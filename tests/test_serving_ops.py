@@ -1312,3 +1312,21 @@ def test_captured_chunk_attn_follows_the_lengths(ksa, N):
             at += m
         assert bool((out[at:] == 5.0).all()) and int(st) == 0
     del graph
+
+
+def test_serving_calls_refuse_numbers_past_32_bits(ksa):
+    """Numbers that the library takes as 32 bits are not cut off: 2^32 + 16 is no block size."""
+    far = 1 << 32
+    table, free, one = i32([[0, 1]]), i32([0, 1, 2]), i32([1])
+    assign = lambda **kw: ksa.ksa_assign_pages(**{**dict(
+        ctx_lens=one, new_lens=one, block_table=table, free_pages=free, num_free=one,
+        block_size=16, num_tokens=2), **kw})
+    q, K = torch.zeros((1, 1, 64), device=DEV).bfloat16(), torch.zeros((1, 1, 4, 64),
+                                                                       device=DEV).bfloat16()
+    for call in (lambda: assign(block_size=far + 16), lambda: assign(num_tokens=far + 2),
+                 lambda: assign(num_tokens=-far - 2),
+                 lambda: ksa.ksa_release_pages(one, one, table, free, one, far + 16),
+                 lambda: ksa.ksa_chunk_attn(q, K, K, i32([0, 1]), one, mask=far + 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+    assert table.tolist() == [[0, 1]] and free.tolist() == [0, 1, 2] and int(one) == 1
